@@ -9,6 +9,7 @@ import re
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libepdc.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "epdc.h")
+EXPERT_HEADER = os.path.join(os.path.dirname(PKG), "include", "epdc_expert.h")
 
 EP_OK = 0
 EP_ERR_INVALID_ARG = -1
@@ -22,6 +23,9 @@ EP_DTYPE_FP8_E4M3 = 1
 EP_SCALE_F32 = 0
 EP_SCALE_POW2 = 1
 EP_SCALE_UE8M0 = 2
+EP_W_BF16 = 0
+EP_W_INT4 = 1
+EP_W_FP4 = 2
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -62,16 +66,33 @@ _SIGNATURES = {
     "ep_combine": (_I32, [_P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _P, _P]),
 }
 
+# include/epdc_expert.h
+_EXPERT_SIGNATURES = {
+    "ep_expert_abi_version": (_I32, []),
+    "ep_quantize_w4": (_I32, [_P, _I64, _I32, _I32, _I32, _P, _P, _P]),
+    "ep_expert_matvec": (
+        _I32, [_P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
+    "ep_moe_tokens_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "ep_moe_tokens": (
+        _I32, [_P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32, _I32, _P,
+               _P, _P, _P, _P, _P, _SZ, _P]),
+    "ep_swiglu_fp8": (_I32, [_P, _I64, _I32, _P, _P, _P, _P, _P]),
+    "ep_swiglu_fp8_backward": (_I32, [_P, _P, _P, _I64, _I32, _P, _P, _P, _P]),
+    "ep_combine_backward": (_I32, [_P, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _P]),
+}
+
 _lib = None
 
 
 # EPDC_ABI_VERSION of include/epdc.h that the signatures above follow
 ABI_VERSION = 6
+# EPDC_EXPERT_ABI_VERSION of include/epdc_expert.h
+EXPERT_ABI_VERSION = 1
 
 
-def header_functions():
-    """Names of the functions declared in include/epdc.h."""
-    with open(HEADER) as f:
+def header_functions(path=HEADER):
+    """Names of the functions declared in include/epdc.h (or another header)."""
+    with open(path) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(ep_[a-z0-9_]+)\s*\(", text)))
@@ -97,7 +118,17 @@ def lib():
             raise ImportError(
                 f"{LIB_PATH} reports ABI version {ver()}, these bindings are for "
                 f"{ABI_VERSION}: rebuild it with `python -m combine_ep_send_amd.build`")
-        for name, (res, args) in _SIGNATURES.items():
+        try:
+            ver = L.ep_expert_abi_version
+        except AttributeError:
+            raise ImportError(f"{LIB_PATH} lacks the expert-side calls: rebuild it with "
+                              "`python -m combine_ep_send_amd.build`")
+        ver.restype, ver.argtypes = _I32, []
+        if ver() != EXPERT_ABI_VERSION:
+            raise ImportError(
+                f"{LIB_PATH} reports expert ABI version {ver()}, these bindings are for "
+                f"{EXPERT_ABI_VERSION}: rebuild it with `python -m combine_ep_send_amd.build`")
+        for name, (res, args) in {**_SIGNATURES, **_EXPERT_SIGNATURES}.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args

@@ -19,7 +19,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libepdc.so")
-SOURCES = ["scan.hip", "fused.hip", "rows.hip", "api.hip"]
+SOURCES = ["scan.hip", "fused.hip", "rows.hip", "api.hip", "expert.hip", "grad.hip",
+           "expert_api.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -12,6 +12,7 @@ from typing import Callable, List, NamedTuple, Optional, Tuple
 
 import torch
 
+from .expert import ep_combine_backward
 from .ops import (Counts, Regrouped, SendLayout, ep_batched_prepare, ep_batched_prepare_fp8,
                   ep_build_send_layout, ep_combine, ep_compute_send_counts,
                   ep_counts_workspace_bytes, ep_dispatch_layout, ep_dispatch_layout_chunked,
@@ -26,6 +27,8 @@ __all__ = [
     "DispatchHandle",
     "dispatch",
     "combine",
+    "combine_backward",
+    "dispatch_backward",
     "dispatch_chunked_forward",
     "ChunkedDispatcher",
     "batched_prepare",
@@ -130,6 +133,23 @@ def combine(local_out: torch.Tensor, handle: DispatchHandle,
     before the one rounding to bf16 (Buffer.combine bias)."""
     return ep_combine(local_out, handle.token_row, handle.topk_weights if weighted else None,
                       bias=bias, out=out)
+
+
+def combine_backward(dout: torch.Tensor, local_out: torch.Tensor, handle: DispatchHandle, *,
+                     weighted: bool = True, d_local_out: Optional[torch.Tensor] = None):
+    """Gradient of ``combine``: (d_local_out, shaped as local_out; the top-k
+    weights' gradient [T,K] fp32, None unweighted).  Rows past the layout's
+    pairs are left as they are in a ``d_local_out`` that is passed, zero in one
+    allocated here."""
+    return ep_combine_backward(dout, local_out, handle.token_row,
+                               handle.topk_weights if weighted else None, dy=d_local_out)
+
+
+def dispatch_backward(d_recv: torch.Tensor, handle: DispatchHandle,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of ``dispatch`` with bf16 rows: each token's sum of the
+    gradients of its send rows (fp32, rounded once to bf16)."""
+    return ep_combine(d_recv, handle.token_row, None, out=out)
 
 
 class ChunkedDispatcher:
