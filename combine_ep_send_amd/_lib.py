@@ -72,7 +72,7 @@ _EXPERT_SIGNATURES = {
     "ep_quantize_w4": (_I32, [_P, _I64, _I32, _I32, _I32, _P, _P, _P]),
     "ep_expert_matvec": (
         _I32, [_P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
-    "ep_moe_tokens_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "ep_moe_tokens_workspace_bytes": (_SZ, [_I64, _I32, _I32, _I32]),
     "ep_moe_tokens": (
         _I32, [_P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32, _I32, _P,
                _P, _P, _P, _P, _P, _SZ, _P]),

@@ -7,15 +7,17 @@
 // v_mfma_f32_16x16x32_bf16 takes up to 16 rows at the cost of one, sums
 // over the lanes by itself and leaves the vector unit to the 4-bit decoding.
 //
-// A wave owns 16*NT weight rows n and walks blocks of 128 channels.  Lane l
-// holds row l % 16 of each tile and the lane group g = l / 16 a quarter of the
-// block's channels.  Loads are 16 bytes a lane through buffer descriptors
-// whose range check returns zeros for the rows past N, the token rows past
-// the expert's count and the channels past K, so nothing branches.  Loads
-// return in order, hence the rows x are fetched as far ahead as the weights:
-// both sit in a ring of D blocks of registers.
+// A wave owns 16*NT weight rows n and walks along the channels in stages of
+// NV*64 bytes of each row.  Loads are 16 bytes a lane through buffer
+// descriptors whose range check returns zeros for the rows past N, the token
+// rows past the expert's count and the channels past K, so nothing branches.
+// Loads return in order, hence the rows x are fetched as far ahead as the
+// weights: both sit in a ring of D stages of registers, and x goes through LDS
+// on its way to the matrix cores.
 #include "epdc_device.h"
 #include "expert_launch.h"
+
+#include <type_traits>
 
 namespace epdc {
 
@@ -26,15 +28,11 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 constexpr uint32_t kOob = 0x80000000u;      // past every descriptor's range (< 2^31 bytes)
-constexpr int kBlockK = 128;                // channels per block
+constexpr int kNonTemporal = 2;             // cache policy bit of the buffer loads
 
 __device__ __forceinline__ rsrc_t make_rsrc(const void* p, int64_t bytes) {
   // stride 0, 32-bit data format: offsets are bytes, checked against `bytes`
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(bytes), 0x00027000);
-}
-
-__device__ __forceinline__ u32x4 load16(rsrc_t r, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
 }
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
@@ -42,33 +40,33 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Bytes of one weight row and of its scales.
+template <int KIND>
+constexpr bool kIsInt4 = KIND == kWInt4G32 || KIND == kWInt4G64 || KIND == kWInt4G128;
+
+// Channels of a 16-byte vector's 64-byte share of a row: 32 bf16 or 128 4-bit.
+template <int KIND>
+constexpr int kVecK = KIND == kWBf16 ? 32 : 128;
+
+// Bytes of one weight row and of its scales, and scale bytes per 128 channels.
 template <int KIND>
 __device__ __forceinline__ int row_bytes(int K) { return KIND == kWBf16 ? 2 * K : K / 2; }
 template <int KIND>
-__device__ __forceinline__ int scale_bytes(int K) {
-  return KIND == kWFp4 ? K / 32
-                       : KIND == kWInt4G32 ? K / 16
-                                           : KIND == kWInt4G64 ? K / 32 : K / 64;
-}
+constexpr int kScaleBytes =
+    KIND == kWFp4 ? 4 : KIND == kWInt4G32 ? 8 : KIND == kWInt4G64 ? 4 : 2;
+template <int KIND>
+__device__ __forceinline__ int scale_bytes(int K) { return K / 128 * kScaleBytes<KIND>; }
 
-// Which channels a lane group holds.  A lane's 16 bytes are 8 channels of a
-// bf16 row but 32 of a 4-bit row.  One matrix instruction sums over all four
-// lane groups, so a scale that differs between them has to be applied before
-// it (fp4: a power of two, exact in bf16) or the lanes have to share it:
-// int4 with one scale per 128 channels does; with 32 or 64 the four dwords
-// are transposed between the lane groups first, which leaves instruction j
-// with the channels 32j..32j+31.  kSplit: group g holds channels 32g..32g+31
-// and instruction j their j-th eight; otherwise group g holds the g-th eight
-// of instruction j's 32 channels.
+// Which channels a lane group (the lanes 16g..16g+15) holds.  A lane's 16
+// bytes are 8 channels of a bf16 row but 32 of a 4-bit row.  One matrix
+// instruction sums over all four lane groups, so a scale that differs between
+// them has to be applied before it (fp4: a power of two, exact in bf16) or the
+// lanes have to share it: int4 with one scale per 128 channels does; with 32
+// or 64 the four dwords are transposed between the lane groups first, which
+// leaves instruction j with the channels 32j..32j+31.  kSplit: group g holds
+// channels 32g..32g+31 and instruction j their j-th eight; otherwise group g
+// holds the g-th eight of instruction j's 32 channels.
 template <int KIND>
 constexpr bool kSplit = KIND == kWFp4 || KIND == kWInt4G128;
-
-template <int KIND>
-struct RawW {
-  u32x4 v[KIND == kWBf16 ? 4 : 1];
-  uint32_t s0, s1;
-};
 
 // The 4x4 transposition of dwords between lane groups: dword j of group g
 // becomes dword g of group j (row swaps of the two bits of g against j's).
@@ -78,6 +76,24 @@ __device__ __forceinline__ u32x4 transpose_groups(u32x4 v) {
   auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
   auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
   return u32x4{c[0], c[1], d[0], d[1]};
+}
+
+// out[b]: the word that lane group b (of the first NV) holds, in every group.
+template <int NV>
+__device__ __forceinline__ void spread_groups(uint32_t w, uint32_t (&out)[NV]) {
+  if constexpr (NV == 4) {
+    auto h = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    auto lo = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    auto hi = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    out[0] = lo[0];
+    out[1] = lo[1];
+    out[2] = hi[0];
+    out[3] = hi[1];
+  } else {                       // two groups hold each word already
+    auto p = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    out[0] = p[0];
+    out[1] = p[1];
+  }
 }
 
 // Eight e2m1 codes times a power of two, as bf16 (exact: two significant
@@ -98,152 +114,284 @@ __device__ __forceinline__ u32x4 decode_fp4(uint32_t d, float scale) {
 // so the product with the row is this one's minus 24 times the row's sum,
 // which another matrix instruction gives for all the tiles of a block.
 __device__ __forceinline__ u32x4 decode_int4(uint32_t d) {
-  constexpr uint32_t m = 0x00780078u, b = 0x41804180u;
+  uint32_t m = 0x00780078u, b = 0x41804180u;
+  // both constants in registers: mask and merge are then one instruction
+  asm("" : "+v"(m));
+  asm("" : "+s"(b));
   return u32x4{((d << 3) & m) | b, ((d >> 1) & m) | b, ((d >> 5) & m) | b, ((d >> 9) & m) | b};
 }
 constexpr uint32_t kMinus24 = 0xC1C0C1C0u;
 
 // A row's eight channels in that order.
-__device__ __forceinline__ u32x4 order_int4(u32x4 x) {
+template <int KIND>
+__device__ __forceinline__ u32x4 order_x(u32x4 x) {
+  if constexpr (!kIsInt4<KIND>) return x;
   return u32x4{__builtin_amdgcn_perm(x.z, x.x, 0x05040100u),
                __builtin_amdgcn_perm(x.z, x.x, 0x07060302u),
                __builtin_amdgcn_perm(x.w, x.y, 0x05040100u),
                __builtin_amdgcn_perm(x.w, x.y, 0x07060302u)};
 }
 
-// Sums of the blocks kb0, kb0 + step, ... below kb1 into acc: MT tiles of 16
-// rows x against NT tiles of 16 weight rows.  xoff, woff and soff are the
-// lane's byte offsets of its row (kOob: none), without the lane group's part.
-// A row x is the sum of XP bf16 rows, `plane` bytes apart.
-template <int KIND, int NT, int MT, int XP, int D>
-__device__ __forceinline__ void few_tile(rsrc_t xr, rsrc_t wr, rsrc_t sr,
-                                         const uint32_t (&xoff)[MT], const uint32_t (&woff)[NT],
-                                         const uint32_t (&soff)[NT], uint32_t plane, int K,
-                                         int kb0, int kb1, int step, f32x4 (&acc)[MT][NT]) {
-  constexpr int WV = KIND == kWBf16 ? 4 : 1;
-  const int g = lane_id() >> 4;
-  RawW<KIND> wb[D][NT];
-  u32x4 xb[D][MT][XP * 4];
+// ---------------------------------------------------------------------------
+// A stage of weights: NV 16-byte vectors a lane of each tile of 16 rows.
+// Vector q of lane group g is bytes 64q + 16g.. of the stage, but a load that
+// takes 64 bytes of 16 rows moves memory at 4.1-5 TB/s where one that takes 128
+// bytes of 8 rows, non-temporal, moves it at 6.1 (a plain 125 MB read; the
+// non-temporal hint with 64 bytes is the slowest of all).  So a pair of
+// vectors is loaded as rows 0-7 and rows 8-15, the lanes n >= 8 of a tile
+// taking the second vector's share, and the halves change places afterwards.
+// One scale load covers the stage, lane group g taking vector g's: loaded
+// vector by vector, the few bytes of each row cost more requests than the
+// weights (fp4 at 7168 channels: 38 against 26 us).
+// ---------------------------------------------------------------------------
+template <int KIND, int NT, int NV>
+struct Stage {
+  u32x4 v[NT][NV];
+  uint32_t s[NT][2];
+};
 
-  auto load = [&](int d, int kb) {
-    const bool in = kb < kb1;
+// A lane's byte offsets into a matrix (kOob: no such row), its share of the
+// stage included: its two weight rows and its scale row of each tile.
+template <int NT>
+struct Rows {
+  uint32_t w[NT][2];
+  uint32_t s[NT];
+};
+
+// Tiles of output channels c0.. below `limit`, `tiles` of them before the next
+// set (the up rows); tile t starts at matrix row tile_row(t).
+template <int KIND, int NT, int NV, typename TileRow>
+__device__ __forceinline__ void set_rows(Rows<NT>& r, int K, TileRow tile_row, int c0, int limit,
+                                         int tiles) {
+  const int n = lane_id() & 15, g = lane_id() >> 4;
+  const int wrow = row_bytes<KIND>(K), srow = scale_bytes<KIND>(K);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+  for (int nt = 0; nt < NT; ++nt) {
+    const int c = c0 + (nt % tiles) * 16;              // output channel of the tile's row 0
 #pragma unroll
-      for (int j = 0; j < WV; ++j) {
-        const bool ok = in && (KIND != kWBf16 || kb * kBlockK + j * 32 + g * 8 < K);
-        const uint32_t off = KIND == kWBf16 ? woff[nt] + uint32_t(kb * 256 + j * 64 + g * 16)
-                                            : woff[nt] + uint32_t(kb * 64 + g * 16);
-        wb[d][nt].v[j] = load16(wr, ok ? off : kOob);
-      }
-      if constexpr (KIND == kWFp4) {
-        wb[d][nt].s0 = uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(
-            sr, in ? soff[nt] + uint32_t(kb * 4 + g) : kOob, 0, 0)));
-      } else if constexpr (KIND == kWInt4G128) {
-        wb[d][nt].s0 = uint32_t(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(
-            sr, in ? soff[nt] + uint32_t(kb * 2) : kOob, 0, 0)));
-      } else if constexpr (KIND == kWInt4G64) {
-        wb[d][nt].s0 =
-            __builtin_amdgcn_raw_buffer_load_b32(sr, in ? soff[nt] + uint32_t(kb * 4) : kOob, 0, 0);
+    for (int h = 0; h < 2; ++h) {
+      const int k = (n & 7) + 8 * h;
+      r.w[nt][h] = c + k < limit ? uint32_t(tile_row(nt) + k) * uint32_t(wrow) +
+                                       uint32_t((n >> 3) * 64 + g * 16)
+                                 : kOob;
+    }
+    r.s[nt] = c + n < limit ? uint32_t(tile_row(nt) + n) * uint32_t(srow) +
+                                  uint32_t((g & (NV - 1)) * kScaleBytes<KIND>)
+                            : kOob;
+  }
+}
+
+// Stage `st` of the rows, or zeros if it is not `in`.  The stage's offset is
+// the same for every lane and goes into the scalar offset; what remains a
+// lane's business is whether its channels lie below K.
+template <int KIND, int NT, int NV>
+__device__ __forceinline__ void load_stage(Stage<KIND, NT, NV>& stage, rsrc_t wr, rsrc_t sr,
+                                           const Rows<NT>& rows, int K, int st, bool in) {
+  const int g = lane_id() >> 4, up = (lane_id() >> 3) & 1;
+  const int left = in ? K - st * (NV * kVecK<KIND>) : 0;         // channels from the stage on
+  const int so = in ? st * (NV * 64) : 0;
+  const int ss = in ? st * (NV * kScaleBytes<KIND>) : 0;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < NV; i += 2) {
+      const bool ok = (i + up) * kVecK<KIND> + (KIND == kWBf16 ? g * 8 : 0) < left;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        stage.v[nt][i + h] = __builtin_amdgcn_raw_buffer_load_b128(
+            wr, (ok ? rows.w[nt][h] : kOob) + i * 64, so, kNonTemporal);
+    }
+    if constexpr (KIND != kWBf16) {
+      const uint32_t off = (g & (NV - 1)) * 128 < left ? rows.s[nt] : kOob;
+      if constexpr (KIND == kWInt4G128) {
+        stage.s[nt][0] = uint32_t(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(sr, off, ss, 0)));
       } else if constexpr (KIND == kWInt4G32) {
-        const auto s =
-            __builtin_amdgcn_raw_buffer_load_b64(sr, in ? soff[nt] + uint32_t(kb * 8) : kOob, 0, 0);
-        wb[d][nt].s0 = s[0];
-        wb[d][nt].s1 = s[1];
+        const auto sc = __builtin_amdgcn_raw_buffer_load_b64(sr, off, ss, 0);
+        stage.s[nt][0] = sc[0];
+        stage.s[nt][1] = sc[1];
+      } else {
+        stage.s[nt][0] = __builtin_amdgcn_raw_buffer_load_b32(sr, off, ss, 0);
       }
     }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = kSplit<KIND> ? g * 32 + j * 8 : j * 32 + g * 8;
-        const bool ok = in && (KIND != kWBf16 || kb * kBlockK + c < K);
-        const uint32_t off = xoff[mt] + uint32_t((kb * kBlockK + c) * 2);
-#pragma unroll
-        for (int p = 0; p < XP; ++p)
-          xb[d][mt][p * 4 + j] = load16(xr, ok ? off + p * plane : kOob);
-      }
-  };
+  }
+}
 
-  auto compute = [&](int d) {
+// The halves of a pair of loads change places: lanes n < 8 give their part of
+// row n + 8 to lane n + 8 and get the second vector of their own row.
+__device__ __forceinline__ void exchange_halves(u32x4& a, u32x4& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    constexpr int kRor8 = 0x128;                       // rotate by 8 within 16 lanes
+    const int x = int(a[i]), y = int(b[i]);
+    a[i] = uint32_t(__builtin_amdgcn_update_dpp(x, y, kRor8, 0xF, 0xC, false));
+    b[i] = uint32_t(__builtin_amdgcn_update_dpp(y, x, kRor8, 0xF, 0x3, false));
+  }
+}
+
+// A stage's products into acc: MT tiles of 16 rows x against NT tiles of 16
+// weight rows.  A row x is the sum of XP bf16 rows.  x(mt, p, q, j): the
+// fragment of row tile mt, part p, for product j of vector q (bf16: q alone),
+// as order_x leaves it; use(mt): whether the tile has rows at all.
+template <int KIND, int NT, int NV, int MT, int XP, typename X, typename Use>
+__device__ __forceinline__ void stage_products(Stage<KIND, NT, NV>& st, X x, Use use,
+                                               f32x4 (&acc)[MT][NT]) {
+  uint32_t s0[NT][NV], s1[NT][NV];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int q = 0; q < NV; q += 2) exchange_halves(st.v[nt][q], st.v[nt][q + 1]);
+    if constexpr (KIND != kWBf16) spread_groups<NV>(st.s[nt][0], s0[nt]);
+    if constexpr (KIND == kWInt4G32) spread_groups<NV>(st.s[nt][1], s1[nt]);
+  }
+#pragma unroll
+  for (int q = 0; q < NV; ++q) {
     if constexpr (KIND == kWBf16) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int mt = 0; mt < MT; ++mt) {
+        if (!use(mt)) continue;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int p = 0; p < XP; ++p) {
+          const u32x4 a = x(mt, p, q, 0);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int p = 0; p < XP; ++p)
-              acc[mt][nt] = mfma(xb[d][mt][p * 4 + j], wb[d][nt].v[j], acc[mt][nt]);
-    } else if constexpr (KIND == kWFp4) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float sc = __uint_as_float(wb[d][nt].s0 << 23);
-        const u32x4 v = wb[d][nt].v[0];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4 b = decode_fp4(v[j], sc);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int p = 0; p < XP; ++p)
-              acc[mt][nt] = mfma(xb[d][mt][p * 4 + j], b, acc[mt][nt]);
+          for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = mfma(a, st.v[nt][q], acc[mt][nt]);
         }
       }
-    } else {
-      constexpr int Q = KIND == kWInt4G128 ? 1 : KIND == kWInt4G64 ? 2 : 4;   // groups a block
-      constexpr int J = 4 / Q;                                                // products a group
-      const u32x4 minus = {kMinus24, kMinus24, kMinus24, kMinus24};
-      u32x4 x[MT][XP * 4];
-      f32x4 base[MT][Q];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          base[mt][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = q * J; j < q * J + J; ++j)
-#pragma unroll
-            for (int p = 0; p < XP; ++p) {
-              x[mt][p * 4 + j] = order_int4(xb[d][mt][p * 4 + j]);
-              base[mt][q] = mfma(x[mt][p * 4 + j], minus, base[mt][q]);
-            }
-        }
+    } else if constexpr (KIND == kWFp4) {
+      u32x4 b[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const u32x4 v =
-            KIND == kWInt4G128 ? wb[d][nt].v[0] : transpose_groups(wb[d][nt].v[0]);
-        u32x4 b[4];
+        const uint32_t byte = s0[nt][q] >> ((lane_id() >> 4) * 8);   // lane group g: byte g
+        const float sc = __uint_as_float((byte << 23) & 0x7F800000u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = decode_int4(v[j]);
+        for (int j = 0; j < 4; ++j) b[nt][j] = decode_fp4(st.v[nt][q][j], sc);
+      }
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          const uint32_t sw = q < 2 ? wb[d][nt].s0 : wb[d][nt].s1;
-          const float sc = Q > 1 && (q & 1) ? bf16_hi(sw) : bf16_lo(sw);
+      for (int mt = 0; mt < MT; ++mt) {
+        if (!use(mt)) continue;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            f32x4 part = base[mt][q];
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = q * J; j < q * J + J; ++j)
+          for (int p = 0; p < XP; ++p) {
+            const u32x4 a = x(mt, p, q, j);
 #pragma unroll
-              for (int p = 0; p < XP; ++p) part = mfma(x[mt][p * 4 + j], b[j], part);
+            for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = mfma(a, b[nt][j], acc[mt][nt]);
+          }
+      }
+    } else {
+      constexpr int Q = KIND == kWInt4G128 ? 1 : KIND == kWInt4G64 ? 2 : 4;   // groups a vector
+      constexpr int J = 4 / Q;                                                // products a group
+      const u32x4 minus = {kMinus24, kMinus24, kMinus24, kMinus24};
+      u32x4 b[NT][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[mt][nt][i] = __builtin_fmaf(sc, part[i], acc[mt][nt][i]);
+      for (int nt = 0; nt < NT; ++nt) {
+        const u32x4 v = kSplit<KIND> ? st.v[nt][q] : transpose_groups(st.v[nt][q]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[nt][j] = decode_int4(v[j]);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        if (!use(mt)) continue;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+          f32x4 base = {0.f, 0.f, 0.f, 0.f};
+          u32x4 a[J][XP];
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int p = 0; p < XP; ++p) {
+              a[j][p] = x(mt, p, q, i * J + j);
+              base = mfma(a[j][p], minus, base);
+            }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            f32x4 part = base;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+              for (int p = 0; p < XP; ++p) part = mfma(a[j][p], b[nt][i * J + j], part);
+            const uint32_t sw = i < 2 ? s0[nt][q] : s1[nt][q];
+            const float sc = Q > 1 && (i & 1) ? bf16_hi(sw) : bf16_lo(sw);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              acc[mt][nt][k] = __builtin_fmaf(sc, part[k], acc[mt][nt][k]);
           }
         }
       }
     }
-  };
+  }
+}
 
+// ---------------------------------------------------------------------------
+// Up to four rows x for one wave alone: the stage's channels of the rows go
+// through an LDS corner of the wave's own, 128 channels of all four a load.
+// Rows past the fourth of a fragment repeat the four, and their products are
+// not used.  A wave's LDS accesses stay in order, so no barrier is needed.
+// ---------------------------------------------------------------------------
+constexpr int kFewRows = 4;
+
+// Blocks of 128 channels of x a stage needs.
+template <int KIND, int NV>
+constexpr int kXBlocks = KIND == kWBf16 ? NV / 4 : NV;
+// 16-byte pieces from row to row: the four rows and four lane groups that a
+// fragment reads at once then lie in different banks.
+template <int KIND>
+constexpr int kXPitch = kSplit<KIND> ? 17 : 20;
+template <int KIND, int NV, int XP>
+constexpr int kXPieces = kXBlocks<KIND, NV> * XP * kFewRows * kXPitch<KIND>;
+
+template <int KIND, int NT, int NV, int XP, int D>
+__device__ __forceinline__ void own_tile(rsrc_t xr, uint32_t xoff, int plane, u32x4* xs,
+                                         rsrc_t wr, rsrc_t sr, const Rows<NT>& rows, int K, int st0,
+                                         int st1, int step, f32x4 (&acc)[1][NT]) {
+  constexpr int XB = kXBlocks<KIND, NV>;
+  static_assert(KIND != kWBf16 || NV % 4 == 0, "a stage holds whole blocks of x");
+  const int lane = lane_id();
+  Stage<KIND, NT, NV> w[D];
+  u32x4 xb[D][XB][XP];
+  auto load = [&](int d, int st) {
+    const bool in = st < st1;
+    const int left = in ? K - st * (NV * kVecK<KIND>) : 0;
+    const int so = in ? st * (NV * kVecK<KIND> * 2) : 0;
+    // xoff: the lane's piece (lane % 16) of 128 channels of row lane / 16
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(d, kb0 + d * step);
-  for (int kb = kb0; kb < kb1; kb += D * step) {
+    for (int b = 0; b < XB; ++b) {
+      const uint32_t off = (b * 128 + (lane & 15) * 8 < left ? xoff : kOob) + b * 256;
+#pragma unroll
+      for (int p = 0; p < XP; ++p)
+        xb[d][b][p] = __builtin_amdgcn_raw_buffer_load_b128(xr, off, so + p * plane, 0);
+    }
+    load_stage<KIND, NT, NV>(w[d], wr, sr, rows, K, st, in);
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    load(d, st0 + d * step);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int st = st0; st < st1; st += D * step) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      compute(d);
-      load(d, kb + (d + D) * step);
+#pragma unroll
+      for (int b = 0; b < XB; ++b)
+#pragma unroll
+        for (int p = 0; p < XP; ++p)
+          xs[((b * XP + p) * kFewRows + (lane >> 4)) * kXPitch<KIND> + (lane & 15)] =
+              order_x<KIND>(xb[d][b][p]);
+      __builtin_amdgcn_wave_barrier();
+      stage_products<KIND, NT, NV, 1, XP>(
+          w[d],
+          [&](int, int p, int q, int j) {
+            const int g = lane >> 4;
+            const int b = KIND == kWBf16 ? q / 4 : q, i = KIND == kWBf16 ? q % 4 : j;
+            const int piece = kSplit<KIND> ? g * 4 + i : i * 4 + g;
+            return xs[((b * XP + p) * kFewRows + (lane & 3)) * kXPitch<KIND> + piece];
+          },
+          [](int) { return true; }, acc);
+      __builtin_amdgcn_wave_barrier();
+      // kept in this order, so that a stage's wait leaves the later stages'
+      // loads in flight
+      __builtin_amdgcn_sched_barrier(0);
+      load(d, st + (d + D) * step);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
@@ -275,13 +423,14 @@ struct SharedPlan {
 
 // Returns the number of slots of the y-th expert in use, 0 if there is none;
 // `first`: the slots of lower experts; `active`: experts in use.
+template <int BLOCK>
 __device__ __forceinline__ int find_expert(SharedPlan& sp, const FewArgs& a, int y, int& expert,
                                            int& first, int& active) {
   const int tid = threadIdx.x;
   const int lane = lane_id();
   if (tid < kFewExperts / 32) sp.bits[tid] = 0u;
   __syncthreads();
-  for (int s = tid; s < a.slots; s += kBlock) {
+  for (int s = tid; s < a.slots; s += BLOCK) {
     const int e = slot_expert(a.ids64, a.ids32, a.first_expert, a.experts, s);
     sp.id[s] = int16_t(e);
     if (e >= 0) atomicOr(&sp.bits[e >> 5], 1u << (e & 31));
@@ -317,211 +466,371 @@ __device__ __forceinline__ int find_expert(SharedPlan& sp, const FewArgs& a, int
   return m;
 }
 
-// ---------------------------------------------------------------------------
-// Few rows against their experts' matrices: grid (tiles of weight rows,
-// experts in use at most).  The four waves of a workgroup take every fourth
-// block of channels each and add up through LDS in a fixed order.  GATED: a
-// tile is half gate and half up rows and y = silu(g) * u.
-// ---------------------------------------------------------------------------
-template <int KIND, int NT, int MT, bool GATED, int D>
-__global__ __launch_bounds__(kBlock) void few_rows_kernel(FewArgs a) {
-  constexpr int C = GATED ? NT / 2 : NT;             // tiles of output channels
-  constexpr int kRow = NT * 16 + 4;                  // + 4: the lane groups' rows in other banks
-  __shared__ SharedPlan sp;
-  __shared__ float red[kWavesPerBlock][MT * 16][kRow];
-  const int lane = lane_id(), wave = wave_id();
-  int e = 0, first = 0, active = 0;
-  int m = find_expert(sp, a, blockIdx.y, e, first, active);
-  e = __builtin_amdgcn_readfirstlane(e);
-  m = __builtin_amdgcn_readfirstlane(m);
-  if (GATED && blockIdx.x == 0) {
-    if (blockIdx.y == 0 && threadIdx.x == 0) a.plan->active = active;
-    if (m > 0 && threadIdx.x == 0) {
+// Zeros for the rows that name no expert, C channels from n0 on.
+template <int C, int BLOCK>
+__device__ __forceinline__ void zero_unnamed(const SharedPlan& sp, const FewArgs& a, int n0) {
+  for (int i = threadIdx.x; i < a.slots * C; i += BLOCK) {
+    const int s = i / C, c = n0 + i % C;
+    if (sp.id[s] < 0 && c < a.N) static_cast<__bf16*>(a.y)[int64_t(s) * a.N + c] = __bf16(0.0f);
+  }
+}
+
+// A layer's first launch leaves the plan for the second.
+template <int BLOCK>
+__device__ __forceinline__ void write_plan(const SharedPlan& sp, const FewArgs& a, int e, int first,
+                                           int m, int active) {
+  if (threadIdx.x == 0) {
+    if (blockIdx.y == 0) a.plan->active = active;
+    if (m > 0) {
       a.plan->expert[blockIdx.y] = e;
       a.plan->first[blockIdx.y] = first;
       a.plan->count[blockIdx.y] = m;
     }
-    for (int i = threadIdx.x; i < m; i += kBlock) a.plan->order[first + i] = sp.list[i];
   }
+  for (int i = threadIdx.x; i < m; i += BLOCK) a.plan->order[first + i] = sp.list[i];
+}
+
+// h = silu(g) * u in two bf16 parts, 16 significant bits together: bf16 alone
+// would double the squared error of the layer's output.  The first part is
+// cut, not rounded, so that it stays finite where h is.
+__device__ __forceinline__ void store_h(__bf16* row, int64_t N, float g, float u) {
+  const float v = g / (1.0f + __expf(-g)) * u;
+  const bool finite = __builtin_fabsf(v) < __builtin_inff();
+  const __bf16 hi =
+      finite ? __bf16(__uint_as_float(__float_as_uint(v) & 0xFFFF0000u)) : __bf16(v);
+  row[0] = hi;
+  row[N] = __bf16(finite ? v - float(hi) : 0.0f);
+}
+
+// What the first launch and the row call write.
+enum : int { kOutGated = 0, kOutBf16 = 1, kOutF32 = 2 };
+
+// Descriptors of expert e's matrix and its scales.
+template <int KIND>
+__device__ __forceinline__ rsrc_t matrix_rsrc(const Weights& w, int e, int rows, int K) {
+  const int64_t bytes = int64_t(rows) * row_bytes<KIND>(K);
+  return make_rsrc(static_cast<const char*>(w.q) + e * bytes, bytes);
+}
+template <int KIND>
+__device__ __forceinline__ rsrc_t scale_rsrc(const Weights& w, int e, int rows, int K) {
+  if (KIND == kWBf16) return make_rsrc(w.q, 0);        // not read
+  const int64_t bytes = int64_t(rows) * scale_bytes<KIND>(K);
+  return make_rsrc(static_cast<const char*>(w.scale) + e * bytes, bytes);
+}
+
+// ---------------------------------------------------------------------------
+// Up to four rows an expert at a time: grid (tiles of weight rows, experts in
+// use at most).  The four waves of a workgroup take every fourth stage of the
+// channels each, which spreads a small matrix over more of the chip, and add
+// up through LDS in a fixed order.  kOutGated: a tile is half gate and half up
+// rows.
+// ---------------------------------------------------------------------------
+template <int KIND, int NT, int NV, int W, int OUT, int D>
+__global__ __launch_bounds__(W * kWave) void few_thin_kernel(FewArgs a) {
+  constexpr bool GATED = OUT == kOutGated;
+  constexpr int C = GATED ? NT / 2 : NT;               // tiles of output channels
+  __shared__ SharedPlan sp;
+  __shared__ u32x4 xs[W][kXPieces<KIND, NV, 1>];
+  __shared__ float red[W][kFewRows][NT * 16];
+  const int lane = lane_id(), wave = wave_id();
+  int e = 0, first = 0, active = 0;
+  int m = find_expert<W * kWave>(sp, a, blockIdx.y, e, first, active);
+  e = __builtin_amdgcn_readfirstlane(e);
+  m = __builtin_amdgcn_readfirstlane(m);
+  if (GATED && blockIdx.x == 0) write_plan<W * kWave>(sp, a, e, first, m, active);
+  const int n0 = blockIdx.x * (C * 16);
+  if (!GATED && blockIdx.y == 0) zero_unnamed<C * 16, W * kWave>(sp, a, n0);
   if (m == 0) return;
 
-  const int rows = GATED ? 2 * a.N : a.N;
-  const int wrow = row_bytes<KIND>(a.K), srow = scale_bytes<KIND>(a.K);
-  const int64_t wbytes = int64_t(rows) * wrow, sbytes = int64_t(rows) * srow;
-  const rsrc_t wr = make_rsrc(static_cast<const char*>(a.w.q) + e * wbytes, wbytes);
-  const rsrc_t sr = KIND == kWBf16
-                        ? wr
-                        : make_rsrc(static_cast<const char*>(a.w.scale) + e * sbytes, sbytes);
+  const int all = GATED ? 2 * a.N : a.N;
+  const rsrc_t wr = matrix_rsrc<KIND>(a.w, e, all, a.K);
+  const rsrc_t sr = scale_rsrc<KIND>(a.w, e, all, a.K);
   const rsrc_t xr = make_rsrc(a.x, int64_t(a.rows) * a.K * 2);
-  const int n0 = blockIdx.x * (C * 16);
-  uint32_t woff[NT], soff[NT];
+  Rows<NT> rows;
+  set_rows<KIND, NT, NV>(
+      rows, a.K, [&](int nt) { return n0 + (nt % C) * 16 + (nt >= C ? a.N : 0); }, n0, a.N, C);
+  const int stages = (a.K + NV * kVecK<KIND> - 1) / (NV * kVecK<KIND>);
+  for (int c0 = 0; c0 < m; c0 += kFewRows) {
+    const int i = c0 + (lane >> 4);
+    const uint32_t xoff = i < m ? uint32_t(sp.list[i] / a.top) * uint32_t(a.K * 2) +
+                                      uint32_t(lane & 15) * 16u
+                                : kOob;
+    f32x4 acc[1][NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int c = n0 + (nt % C) * 16 + (lane & 15);
-    const int r = GATED && nt >= C ? a.N + c : c;
-    woff[nt] = c < a.N ? uint32_t(r) * uint32_t(wrow) : kOob;
-    soff[nt] = c < a.N ? uint32_t(r) * uint32_t(srow) : kOob;
+    for (int nt = 0; nt < NT; ++nt) acc[0][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    own_tile<KIND, NT, NV, 1, D>(xr, xoff, 0, xs[wave], wr, sr, rows, a.K, wave, stages, W, acc);
+    if (c0 > 0) __syncthreads();                       // the last rows' sums have been read
+    if (lane < 16) {                                   // lane l: channel l of rows 0..3
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < kFewRows; ++k) red[wave][k][nt * 16 + lane] = acc[0][nt][k];
+    }
+    __syncthreads();
+    const int mc = m - c0 < kFewRows ? m - c0 : kFewRows;
+    for (int k = threadIdx.x; k < mc * (C * 16); k += W * kWave) {
+      const int r = k / (C * 16), c = k % (C * 16);
+      if (n0 + c >= a.N) continue;
+      float v = 0.f, u = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        v += red[w][r][c];
+        if (GATED) u += red[w][r][C * 16 + c];
+      }
+      const int64_t slot = sp.list[c0 + r];
+      if constexpr (GATED)
+        store_h(static_cast<__bf16*>(a.y) + slot * (2 * a.N) + n0 + c, a.N, v, u);
+      else
+        static_cast<__bf16*>(a.y)[slot * a.N + n0 + c] = __bf16(v);
+    }
   }
-  const int nkb = (a.K + kBlockK - 1) / kBlockK;
+}
+
+__device__ __forceinline__ void lds_barrier() {
+  // LDS accesses done, then the barrier; loads from memory stay in flight
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// ---------------------------------------------------------------------------
+// The same for more rows: the four waves of a workgroup own different weight
+// rows and share the rows x, which each fetches a quarter of and passes on
+// through LDS, stage by stage.  A row x then comes out of the L2 once for
+// 64*NT weight rows.
+// ---------------------------------------------------------------------------
+template <int KIND, int NT, int NV, int MT, int XP, int OUT, int D>
+__global__ __launch_bounds__(kBlock) void few_wide_kernel(FewArgs a) {
+  constexpr bool GATED = OUT == kOutGated;
+  constexpr int C = GATED ? NT / 2 : NT;               // tiles of output channels a wave
+  constexpr int XB = kXBlocks<KIND, NV>;
+  static_assert(D % 2 == 0, "the two buffers of x take turns");
+  __shared__ SharedPlan sp;
+  __shared__ u32x4 xs[2][MT][XP][XB][4][kWave];
+  const int lane = lane_id(), wave = wave_id();
+  int e = 0, first = 0, active = 0;
+  int m = find_expert<kBlock>(sp, a, blockIdx.y, e, first, active);
+  e = __builtin_amdgcn_readfirstlane(e);
+  m = __builtin_amdgcn_readfirstlane(m);
+  if (GATED && blockIdx.x == 0) write_plan<kBlock>(sp, a, e, first, m, active);
+  if (OUT == kOutBf16 && blockIdx.y == 0)
+    zero_unnamed<C * 16 * kWavesPerBlock, kBlock>(sp, a, blockIdx.x * (C * 16 * kWavesPerBlock));
+  if (m == 0) return;
+
+  const int all = GATED ? 2 * a.N : a.N;
+  const rsrc_t wr = matrix_rsrc<KIND>(a.w, e, all, a.K);
+  const rsrc_t sr = scale_rsrc<KIND>(a.w, e, all, a.K);
+  const rsrc_t xr = make_rsrc(a.x, int64_t(a.rows) * a.K * (2 * XP));
+  const int n0 = (blockIdx.x * kWavesPerBlock + wave) * (C * 16);
+  Rows<NT> rows;
+  set_rows<KIND, NT, NV>(
+      rows, a.K, [&](int nt) { return n0 + (nt % C) * 16 + (nt >= C ? a.N : 0); }, n0, a.N, C);
+  const int stages = (a.K + NV * kVecK<KIND> - 1) / (NV * kVecK<KIND>);
   for (int c0 = 0; c0 < m; c0 += 16 * MT) {
+    const int left = m - c0;
+    // this wave fetches product `wave` of every 128 channels: the lane's piece
+    const int piece = kSplit<KIND> ? (lane >> 4) * 4 + wave : wave * 4 + (lane >> 4);
     uint32_t xoff[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int i = c0 + mt * 16 + (lane & 15);
-      xoff[mt] = i < m ? uint32_t(sp.list[i] / a.top) * uint32_t(a.K * 2) : kOob;
+      xoff[mt] = i < m ? uint32_t(sp.list[i] / a.top) * uint32_t(a.K * 2 * XP) +
+                             uint32_t(piece * 16)
+                       : kOob;
     }
     f32x4 acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    few_tile<KIND, NT, MT, 1, D>(xr, wr, sr, xoff, woff, soff, 0u, a.K, wave, nkb,
-                                 kWavesPerBlock, acc);
-    if (c0 > 0) __syncthreads();                     // the last chunk's sums have been read
+    Stage<KIND, NT, NV> w[D];
+    u32x4 xb[D][MT][XP][XB];
+    auto load = [&](int d, int st) {
+      const bool in = st < stages;
+      const int left = in ? a.K - st * (NV * kVecK<KIND>) : 0;
+      const int so = in ? st * (NV * kVecK<KIND> * 2) : 0;
+      const int mine = piece * 8;                      // the lane's channel of every 128
+#pragma unroll
+      for (int b = 0; b < XB; ++b) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint32_t off = (b * 128 + mine < left ? xoff[mt] : kOob) + b * 256;
+#pragma unroll
+          for (int p = 0; p < XP; ++p)
+            xb[d][mt][p][b] =
+                __builtin_amdgcn_raw_buffer_load_b128(xr, off, so + p * (2 * a.K), 0);
+        }
+      }
+      load_stage<KIND, NT, NV>(w[d], wr, sr, rows, a.K, st, in);
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      load(d, d);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int st = 0; st < stages; st += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        // D is even, so that d % 2 alternates over the whole loop: a buffer is
+        // written again only after the barrier that follows its last reads
+        const int buf = d & 1;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int p = 0; p < XP; ++p)
+#pragma unroll
+            for (int b = 0; b < XB; ++b)
+              xs[buf][mt][p][b][wave][lane] = order_x<KIND>(xb[d][mt][p][b]);
+        lds_barrier();
+        stage_products<KIND, NT, NV, MT, XP>(
+            w[d],
+            [&](int mt, int p, int q, int j) {
+              return KIND == kWBf16 ? xs[buf][mt][p][q / 4][q % 4][lane]
+                                    : xs[buf][mt][p][q][j][lane];
+            },
+            [&](int mt) { return mt == 0 || mt * 16 < left; }, acc);
+        __builtin_amdgcn_sched_barrier(0);             // as in own_tile
+        load(d, st + d + D);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    lds_barrier();                                     // the next rows write the first buffer
+    // lane l holds channel l % 16 of rows 4 * (l / 16) + 0..3 of each tile
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int i = 0; i < 4; ++i) {
+        const int r = mt * 16 + (lane >> 4) * 4 + i;
+        if (r >= left) continue;
+        const int64_t slot = sp.list[c0 + r];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          red[wave][mt * 16 + (lane >> 4) * 4 + i][nt * 16 + (lane & 15)] = acc[mt][nt][i];
-    __syncthreads();
-    const int mc = m - c0 < 16 * MT ? m - c0 : 16 * MT;
-    __bf16* y = static_cast<__bf16*>(a.y);
-    for (int i = threadIdx.x; i < mc * (C * 16); i += kBlock) {
-      const int r = i / (C * 16), c = i % (C * 16);
-      if (n0 + c >= a.N) continue;
-      float v = 0.f, u = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWavesPerBlock; ++w) {
-        v += red[w][r][c];
-        if (GATED) u += red[w][r][C * 16 + c];
+        for (int t = 0; t < C; ++t) {
+          const int c = n0 + t * 16 + (lane & 15);
+          if (c >= a.N) continue;
+          if constexpr (OUT == kOutGated)
+            store_h(static_cast<__bf16*>(a.y) + slot * (2 * a.N) + c, a.N, acc[mt][t][i],
+                    acc[mt][C + t][i]);
+          else if constexpr (OUT == kOutBf16)
+            static_cast<__bf16*>(a.y)[slot * a.N + c] = __bf16(acc[mt][t][i]);
+          else
+            static_cast<float*>(a.y)[slot * a.N + c] = acc[mt][t][i];
+        }
       }
-      const int slot = sp.list[c0 + r];
-      if (GATED) {
-        // h in two bf16 parts, 16 significant bits together: bf16 alone would
-        // double the squared error of the layer's output.  The first part is
-        // cut, not rounded, so that it stays finite where h is.
-        v = v / (1.0f + __expf(-v)) * u;
-        const bool finite = __builtin_fabsf(v) < __builtin_inff();
-        const __bf16 hi = finite ? __bf16(__uint_as_float(__float_as_uint(v) & 0xFFFF0000u))
-                                 : __bf16(v);
-        __bf16* h = y + int64_t(slot) * (2 * a.N) + n0 + c;
-        h[0] = hi;
-        h[a.N] = __bf16(finite ? v - float(hi) : 0.0f);
-      } else {
-        y[int64_t(slot) * a.N + n0 + c] = __bf16(v);
-      }
-    }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Second launch of a layer: the down products and the weighted sum.  A
-// workgroup owns 16 output channels of every token, so the sum over a token's
-// experts needs no atomics: its eight waves share out (expert, part of the
-// channels) and leave each slot's products in LDS, then one thread per
+// Second launch of a layer of a few slots: the down products and the weighted
+// sum.  A workgroup owns 16 output channels of every token, so the sum over a
+// token's experts needs no atomics: its eight waves share out (expert, part of
+// the channels) and leave each slot's products in LDS, then one thread per
 // (token, channel) adds them up in the order of the slots.
 // ---------------------------------------------------------------------------
 constexpr int kDownWaves = 8;
 constexpr int kDownBlock = kDownWaves * kWave;
 constexpr int kDownMaxSplit = 8;
+constexpr int kDownSlots = 64;                         // most slots: kFewRows tokens of 16
 
-struct DownShared {
-  int16_t expert[kFewExperts];
-  uint16_t first[kFewExperts];
-  uint16_t count[kFewExperts];
-  uint16_t order[kFewSlots];
-  float w[kFewSlots];
-  uint8_t local[kFewSlots];
-};
-
-template <int KIND, int MT, int D>
-__global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a, int max_split) {
-  __shared__ DownShared ds;
-  extern __shared__ float prod[];                    // [split][slots][16]
+template <int KIND, int NV, int D>
+__global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a) {
+  extern __shared__ float prod[];                      // [split][slots][16]
+  __shared__ u32x4 xs[kDownWaves][kXPieces<KIND, NV, 2>];
+  __shared__ int16_t expert[kDownSlots], order[kDownSlots], first[kDownSlots], count[kDownSlots];
+  __shared__ float weight[kDownSlots];
+  __shared__ uint8_t local[kDownSlots];
   const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
   const int slots = a.T * a.K;
-  const int most = slots < a.experts ? slots : a.experts;
   const int active = a.plan->active;
-  for (int i = tid; i < most; i += kDownBlock) {     // entries past `active` are not used
-    ds.expert[i] = int16_t(a.plan->expert[i]);
-    ds.first[i] = uint16_t(a.plan->first[i]);
-    ds.count[i] = uint16_t(a.plan->count[i]);
-  }
-  for (int i = tid; i < slots; i += kDownBlock) {
-    ds.order[i] = uint16_t(a.plan->order[i]);
-    ds.w[i] = a.topk_weights[i];
-    ds.local[i] = slot_expert(a.ids64, nullptr, a.first_expert, a.experts, i) >= 0;
+  if (tid < slots) {                                   // entries past `active` are not used
+    expert[tid] = int16_t(a.plan->expert[tid]);
+    first[tid] = int16_t(a.plan->first[tid]);
+    count[tid] = int16_t(a.plan->count[tid]);
+    order[tid] = int16_t(a.plan->order[tid]);
+    weight[tid] = a.topk_weights[tid];
+    local[tid] = slot_expert(a.ids64, nullptr, a.first_expert, a.experts, tid) >= 0;
   }
   __syncthreads();
 
-  const int nkb = (a.I + kBlockK - 1) / kBlockK;
+  const int stages = (a.I + NV * kVecK<KIND> - 1) / (NV * kVecK<KIND>);
   // parts per expert: the smallest of 1, 2, 4, 8 that leaves the busiest wave
   // the least to do
   int split = 1;
   {
     int best = (active + kDownWaves - 1) / kDownWaves * kDownMaxSplit;
-    for (int s = 2; s <= max_split && s <= nkb; s *= 2) {
+    for (int s = 2; s <= kDownMaxSplit && s <= stages; s *= 2) {
       const int cost = (active * s + kDownWaves - 1) / kDownWaves * (kDownMaxSplit / s);
       if (cost < best) best = cost, split = s;
     }
   }
   const int n0 = blockIdx.x * 16;
-  const int c = n0 + (lane & 15);
-  const int wrow = row_bytes<KIND>(a.I), srow = scale_bytes<KIND>(a.I);
-  const int64_t wbytes = int64_t(a.H) * wrow, sbytes = int64_t(a.H) * srow;
-  const uint32_t woff[1] = {c < a.H ? uint32_t(c) * uint32_t(wrow) : kOob};
-  const uint32_t soff[1] = {c < a.H ? uint32_t(c) * uint32_t(srow) : kOob};
+  Rows<1> rows;
+  set_rows<KIND, 1, NV>(rows, a.I, [&](int) { return n0; }, n0, a.H, 1);
   const rsrc_t xr = make_rsrc(a.h, int64_t(slots) * a.I * 4);
   for (int u = wave; u < active * split; u += kDownWaves) {
     const int i = u / split, part = u % split;
-    const int e = __builtin_amdgcn_readfirstlane(int(ds.expert[i]));
-    const int m = __builtin_amdgcn_readfirstlane(int(ds.count[i]));
-    const int first = __builtin_amdgcn_readfirstlane(int(ds.first[i]));
-    const rsrc_t wr = make_rsrc(static_cast<const char*>(a.w.q) + e * wbytes, wbytes);
-    const rsrc_t sr = KIND == kWBf16
-                          ? wr
-                          : make_rsrc(static_cast<const char*>(a.w.scale) + e * sbytes, sbytes);
-    for (int c0 = 0; c0 < m; c0 += 16 * MT) {
-      uint32_t xoff[MT];
+    const int e = __builtin_amdgcn_readfirstlane(int(expert[i]));
+    const int m = __builtin_amdgcn_readfirstlane(int(count[i]));
+    const int f = __builtin_amdgcn_readfirstlane(int(first[i]));
+    const rsrc_t wr = matrix_rsrc<KIND>(a.w, e, a.H, a.I);
+    const rsrc_t sr = scale_rsrc<KIND>(a.w, e, a.H, a.I);
+    for (int c0 = 0; c0 < m; c0 += kFewRows) {
+      const int r = c0 + (lane >> 4);
+      const uint32_t xoff =
+          r < m ? uint32_t(order[f + r]) * uint32_t(a.I * 4) + uint32_t(lane & 15) * 16u : kOob;
+      f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
+      own_tile<KIND, 1, NV, 2, D>(xr, xoff, a.I * 2, xs[wave], wr, sr, rows, a.I,
+                                  part * stages / split, (part + 1) * stages / split, 1, acc);
+      if (lane < 16) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int r = c0 + mt * 16 + (lane & 15);
-        xoff[mt] = r < m ? uint32_t(ds.order[first + r]) * uint32_t(a.I * 4) : kOob;
+        for (int k = 0; k < kFewRows; ++k)
+          if (c0 + k < m) prod[(part * slots + order[f + c0 + k]) * 16 + lane] = acc[0][0][k];
       }
-      f32x4 acc[MT][1];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) acc[mt][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-      few_tile<KIND, 1, MT, 2, D>(xr, wr, sr, xoff, woff, soff, uint32_t(a.I * 2), a.I,
-                                  part * nkb / split, (part + 1) * nkb / split, 1, acc);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = c0 + mt * 16 + (lane >> 4) * 4 + j;
-          if (r < m)
-            prod[(part * slots + ds.order[first + r]) * 16 + (lane & 15)] = acc[mt][0][j];
-        }
     }
   }
   __syncthreads();
-  for (int i = tid; i < a.T * 16; i += kDownBlock) {
-    const int t = i >> 4, ch = n0 + (i & 15);
-    if (ch >= a.H) continue;
+  if (tid < a.T * 16 && n0 + (tid & 15) < a.H) {
+    const int t = tid >> 4, ch = n0 + (tid & 15);
     float sum = 0.f;
     for (int k = 0; k < a.K; ++k) {
       const int s = t * a.K + k;
-      if (!ds.local[s]) continue;
+      if (!local[s]) continue;
       float y = 0.f;
-      for (int p = 0; p < split; ++p) y += prod[(p * slots + s) * 16 + (i & 15)];
-      sum += ds.w[s] * y;
+      for (int p = 0; p < split; ++p) y += prod[(p * slots + s) * 16 + (tid & 15)];
+      sum += weight[s] * y;
     }
     const int64_t o = int64_t(t) * a.H + ch;
     if (a.bias0) sum += float(static_cast<const __bf16*>(a.bias0)[o]);
     if (a.bias1) sum += float(static_cast<const __bf16*>(a.bias1)[o]);
     static_cast<__bf16*>(a.out)[o] = __bf16(sum);
   }
+}
+
+// The weighted sum of the slots' products y [slots, H], after the wide form of
+// the down products: one thread per token and four channels.
+__global__ __launch_bounds__(kBlock) void few_sum_kernel(DownArgs a) {
+  const int t = blockIdx.y;
+  const int c = (blockIdx.x * kBlock + threadIdx.x) * 4;
+  if (c >= a.H) return;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < a.K; ++k) {
+    const int s = t * a.K + k;
+    if (slot_expert(a.ids64, nullptr, a.first_expert, a.experts, s) < 0) continue;
+    const float w = a.topk_weights[s];
+    const f32x4 y = *reinterpret_cast<const f32x4*>(a.y + int64_t(s) * a.H + c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] += w * y[i];
+  }
+  const int64_t o = int64_t(t) * a.H + c;
+  for (const void* b : {a.bias0, a.bias1}) {
+    if (!b) continue;
+    const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const __bf16*>(b) + o);
+    sum[0] += bf16_lo(v.x);
+    sum[1] += bf16_hi(v.x);
+    sum[2] += bf16_lo(v.y);
+    sum[3] += bf16_hi(v.y);
+  }
+  *reinterpret_cast<u32x2*>(static_cast<__bf16*>(a.out) + o) =
+      u32x2{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
 }
 
 // ---------------------------------------------------------------------------
@@ -596,53 +905,95 @@ __global__ __launch_bounds__(kBlock) void quantize_w4_kernel(QuantArgs a, int64_
   static_cast<uint32_t*>(a.q)[p] = code;
 }
 
-template <int KIND, bool GATED>
-hipError_t rows_variant(const FewArgs& a, hipStream_t s) {
-  // A first cut: two tiles a wave (a gate and an up tile), 16 rows at a time.
-  constexpr int NT = 2;
-  constexpr int C = GATED ? NT / 2 : NT;
-  const unsigned most = unsigned(a.slots < a.experts ? a.slots : a.experts);
-  const dim3 grid(unsigned((a.N + C * 16 - 1) / (C * 16)), most);
-  few_rows_kernel<KIND, NT, 1, GATED, 2><<<grid, kBlock, 0, s>>>(a);
+// Tuning of the launches.
+template <int KIND> constexpr int kThinNV = KIND == kWBf16 ? 4 : 2;
+template <int KIND> constexpr int kThinD = 2;
+constexpr int kThinW = 4;
+template <int KIND> constexpr int kWideNT = 2;
+template <int KIND> constexpr int kWideNV = KIND == kWBf16 ? 4 : 2;
+template <int KIND> constexpr int kWideD = 2;
+constexpr int kWideMT = 2;
+template <int KIND> constexpr int kDownNV = KIND == kWBf16 ? 4 : 2;
+template <int KIND> constexpr int kDownD = 2;
+
+unsigned most_experts(const FewArgs& a) {
+  return unsigned(a.slots < a.experts ? a.slots : a.experts);
+}
+
+template <int KIND, int OUT>
+hipError_t wide_variant(const FewArgs& a, hipStream_t s) {
+  constexpr int NT = kWideNT<KIND>;
+  constexpr int C = (OUT == kOutGated ? NT / 2 : NT) * 16 * kWavesPerBlock;
+  constexpr int XP = OUT == kOutF32 ? 2 : 1;
+  const dim3 grid(unsigned((a.N + C - 1) / C), most_experts(a));
+  few_wide_kernel<KIND, NT, kWideNV<KIND>, kWideMT, XP, OUT, kWideD<KIND>>
+      <<<grid, kBlock, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <bool GATED>
-hipError_t rows_kind(const FewArgs& a, hipStream_t s) {
-  switch (a.w.kind) {
-    case kWBf16: return rows_variant<kWBf16, GATED>(a, s);
-    case kWFp4: return rows_variant<kWFp4, GATED>(a, s);
-    case kWInt4G32: return rows_variant<kWInt4G32, GATED>(a, s);
-    case kWInt4G64: return rows_variant<kWInt4G64, GATED>(a, s);
-    default: return rows_variant<kWInt4G128, GATED>(a, s);
+template <int KIND, int OUT>
+hipError_t thin_variant(const FewArgs& a, hipStream_t s) {
+  constexpr int NT = OUT == kOutGated ? 2 : 1;
+  constexpr int C = (OUT == kOutGated ? NT / 2 : NT) * 16;
+  const dim3 grid(unsigned((a.N + C - 1) / C), most_experts(a));
+  few_thin_kernel<KIND, NT, kThinNV<KIND>, kThinW, OUT, kThinD<KIND>>
+      <<<grid, kThinW * kWave, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// Calls fn with the weight kind as a compile-time constant.
+template <typename Fn>
+hipError_t with_kind(WeightKind kind, Fn fn) {
+  switch (kind) {
+    case kWBf16: return fn(std::integral_constant<int, kWBf16>());
+    case kWFp4: return fn(std::integral_constant<int, kWFp4>());
+    case kWInt4G32: return fn(std::integral_constant<int, kWInt4G32>());
+    case kWInt4G64: return fn(std::integral_constant<int, kWInt4G64>());
+    default: return fn(std::integral_constant<int, kWInt4G128>());
   }
-}
-
-template <int KIND>
-hipError_t down_variant(const DownArgs& a, hipStream_t s) {
-  // LDS of the products: 64 bytes a slot and part, at most 64 KiB
-  const int slots = a.T * a.K;
-  int split = kDownMaxSplit;
-  while (split > 1 && split * slots > 1024) split >>= 1;
-  few_down_kernel<KIND, 1, 2><<<dim3(unsigned((a.H + 15) / 16)), kDownBlock,
-                                size_t(split) * size_t(slots) * 64, s>>>(a, split);
-  return hipGetLastError();
 }
 
 }  // namespace
 
+bool few_is_wide(int rows) { return rows > kFewRows; }
+
 hipError_t launch_few_rows(const FewArgs& a, bool gated, hipStream_t s) {
-  return gated ? rows_kind<true>(a, s) : rows_kind<false>(a, s);
+  return with_kind(a.w.kind, [&](auto kind) {
+    constexpr int KIND = decltype(kind)::value;
+    if (few_is_wide(a.rows))
+      return gated ? wide_variant<KIND, kOutGated>(a, s) : wide_variant<KIND, kOutBf16>(a, s);
+    return gated ? thin_variant<KIND, kOutGated>(a, s) : thin_variant<KIND, kOutBf16>(a, s);
+  });
 }
 
 hipError_t launch_few_down(const DownArgs& a, hipStream_t s) {
-  switch (a.w.kind) {
-    case kWBf16: return down_variant<kWBf16>(a, s);
-    case kWFp4: return down_variant<kWFp4>(a, s);
-    case kWInt4G32: return down_variant<kWInt4G32>(a, s);
-    case kWInt4G64: return down_variant<kWInt4G64>(a, s);
-    default: return down_variant<kWInt4G128>(a, s);
-  }
+  if (!few_is_wide(a.T))
+    return with_kind(a.w.kind, [&](auto kind) {
+      constexpr int KIND = decltype(kind)::value;
+      few_down_kernel<KIND, kDownNV<KIND>, kDownD<KIND>>
+          <<<dim3(unsigned((a.H + 15) / 16)), kDownBlock,
+             size_t(kDownMaxSplit) * size_t(a.T * a.K) * 64, s>>>(a);
+      return hipGetLastError();
+    });
+  FewArgs f{};
+  f.x = a.h;
+  f.ids64 = a.ids64;
+  f.first_expert = a.first_expert;
+  f.slots = a.T * a.K;
+  f.top = 1;
+  f.rows = f.slots;
+  f.experts = a.experts;
+  f.N = a.H;
+  f.K = a.I;
+  f.w = a.w;
+  f.y = a.y;
+  const hipError_t e = with_kind(a.w.kind, [&](auto kind) {
+    return wide_variant<decltype(kind)::value, kOutF32>(f, s);
+  });
+  if (e != hipSuccess) return e;
+  const dim3 grid(unsigned((a.H / 4 + kBlock - 1) / kBlock), unsigned(a.T));
+  few_sum_kernel<<<grid, kBlock, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 hipError_t launch_quantize_w4(const QuantArgs& a, hipStream_t s) {

@@ -45,6 +45,9 @@ int check_weights(int fmt, int group, int out, int in, const void* w, const void
   return EP_OK;
 }
 
+// The activations h in two bf16 parts, 256-byte aligned at their end.
+size_t h_bytes(size_t slots, int inner) { return (slots * size_t(inner) * 4 + 255) / 256 * 256; }
+
 Weights weights(int fmt, int group, const void* w, const void* scale) {
   const WeightKind kind = fmt == EP_W_BF16 ? kWBf16
                           : fmt == EP_W_FP4 ? kWFp4
@@ -112,12 +115,15 @@ int ep_expert_matvec(const void* x, const int32_t* row_expert, int64_t num_rows,
   return launch_status(launch_few_rows(a, false, stream));
 }
 
-size_t ep_moe_tokens_workspace_bytes(int64_t num_tokens, int num_topk, int inner) {
-  if (num_tokens < 0 || num_topk < 1 || inner < 1) return 0;
+size_t ep_moe_tokens_workspace_bytes(int64_t num_tokens, int num_topk, int hidden, int inner) {
+  if (num_tokens < 0 || num_topk < 1 || hidden < 1 || inner < 1) return 0;
   if (num_tokens > EPDC_FEW_TOKENS || num_topk > EPDC_MAX_TOPK ||
-      num_tokens * num_topk > EPDC_FEW_SLOTS || inner > EPDC_FEW_CHANNELS)
+      num_tokens * num_topk > EPDC_FEW_SLOTS || hidden > EPDC_FEW_CHANNELS ||
+      inner > EPDC_FEW_CHANNELS)
     return 0;
-  return kPlanBytes + size_t(num_tokens) * size_t(num_topk) * size_t(inner) * 4;
+  const size_t slots = size_t(num_tokens) * size_t(num_topk);
+  return kPlanBytes + h_bytes(slots, inner) +
+         (few_is_wide(int(num_tokens)) ? slots * size_t(hidden) * 4 : 0);
 }
 
 int ep_moe_tokens(const void* x, const int64_t* topk_idx, const float* topk_weights,
@@ -144,7 +150,7 @@ int ep_moe_tokens(const void* x, const int64_t* topk_idx, const float* topk_weig
       (bias0 && !aligned(bias0, 16)) || (bias1 && !aligned(bias1, 16)))
     return EP_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) ||
-      workspace_bytes < ep_moe_tokens_workspace_bytes(num_tokens, num_topk, inner))
+      workspace_bytes < ep_moe_tokens_workspace_bytes(num_tokens, num_topk, hidden, inner))
     return EP_ERR_WORKSPACE;
   if (num_tokens == 0) return EP_OK;
   FewPlan* plan = static_cast<FewPlan*>(workspace);
@@ -178,6 +184,7 @@ int ep_moe_tokens(const void* x, const int64_t* topk_idx, const float* topk_weig
   d.bias0 = bias0;
   d.bias1 = bias1;
   d.out = out;
+  d.y = reinterpret_cast<float*>(static_cast<char*>(h) + h_bytes(size_t(a.slots), inner));
   return launch_status(launch_few_down(d, stream));
 }
 

@@ -63,7 +63,11 @@ struct DownArgs {
   const void* bias0;
   const void* bias1;
   void* out;
+  float* y;                        // [slots, H], used by the wide form
 };
+// Whether calls of so many rows (a layer: tokens) take the wide form, whose
+// workspace holds y.
+bool few_is_wide(int rows);
 hipError_t launch_few_down(const DownArgs& a, hipStream_t s);
 
 struct QuantArgs {

@@ -15,8 +15,8 @@ from typing import NamedTuple, Optional, Tuple, Union
 
 import torch
 
-from ._lib import EP_W_BF16, EP_W_FP4, EP_W_INT4, check, lib
-from .ops import _gpu, _shape, _stream, _vp
+from ._lib import EP_OK, EP_W_BF16, EP_W_FP4, EP_W_INT4, check, lib
+from .ops import _gpu, _shape
 
 __all__ = [
     "W4Weights",
@@ -50,54 +50,73 @@ class W4Weights(NamedTuple):
 Weights = Union[torch.Tensor, W4Weights]
 
 
-def _on_device(fn):
-    """Run with the first tensor's device current, and the stream that was
-    given, so that outputs allocated inside belong to both."""
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        if not isinstance(first, torch.Tensor) or first.device.type != "cuda":
-            return fn(first, *args, **kw)              # refused there, by its name
-        if stream is not None:
-            if stream.device != first.device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {first.device}")
-            with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
-        if first.device.index != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
-    return call
+# The calls take microseconds on the GPU, so the host's share counts: a check
+# that passes costs a few attribute reads, and only one that fails goes through
+# the named checks for its message.  The raw handle of the current stream costs
+# a thirtieth of torch.cuda.current_stream() (0.1 against 2.9 us).
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _on(t: torch.Tensor, name: str, dtype, shape, dev) -> torch.Tensor:
-    _shape(_gpu(t, name, dtype), name, shape)
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _first(t, name: str, dtype, ndim: int) -> int:
+    """Checks a call's first tensor and returns its device's index."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim
+            and t.is_contiguous()):
+        _gpu(t, name, dtype, ndim)
+    return t.get_device()
+
+
+def _on(t, name: str, dtype, shape, index: int) -> torch.Tensor:
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous()):
+        _shape(_gpu(t, name, dtype), name, shape)
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
     return t
 
 
-def _weights(w: Weights, name: str, dev):
+def _elsewhere(index: int, stream) -> bool:
+    return stream is not None or index != torch.cuda.current_device()
+
+
+def _there(fn, index: int, stream, *args, **kw):
+    """fn with its tensors' device current, and the stream that was given, so
+    that outputs allocated inside belong to both."""
+    if stream is None:
+        with torch.cuda.device(index):
+            return fn(*args, **kw)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _weights(w: Weights, name: str, index: int):
     """(E, N, K, format, group, q, scale) of bf16 [E, N, K] or W4Weights."""
     if isinstance(w, W4Weights):
-        if w.fmt not in _W4_FMT:
+        q, scale, form, group = w
+        fmt = _W4_FMT.get(form)
+        if fmt is None:
             raise ValueError(f"{name}.fmt must be one of {sorted(_W4_FMT)}")
-        q, group = _gpu(w.q, f"{name}.q", _U8, 3), int(w.group)
+        if _first(q, f"{name}.q", _U8, 3) != index:
+            raise ValueError(f"{name}.q is on {q.device}, not on cuda:{index}")
         E, N, half = q.shape
         if group < 1:
             raise ValueError(f"{name}.group must be positive")
-        _on(w.scale, f"{name}.scale", _W4_SCALE[w.fmt], (E, N, 2 * half // group), dev)
-        out = E, N, 2 * half, _W4_FMT[w.fmt], group, q, w.scale
-    else:
-        q = _gpu(w, name, _BF16, 3)
-        out = (*q.shape, EP_W_BF16, 0, q, None)
-    if q.device != dev:
-        raise ValueError(f"{name} is on {q.device}, not on {dev}")
-    return out
+        _on(scale, f"{name}.scale", _W4_SCALE[form], (E, N, 2 * half // group), index)
+        return E, N, 2 * half, fmt, group, q.data_ptr(), scale.data_ptr()
+    if _first(w, name, _BF16, 3) != index:
+        raise ValueError(f"{name} is on {w.device}, not on cuda:{index}")
+    E, N, K = w.shape
+    return E, N, K, EP_W_BF16, 0, w.data_ptr(), None
 
 
-@_on_device
 def ep_quantize_w4(w: torch.Tensor, fmt: str = "int4", group: Optional[int] = None, *,
-                   out: Optional[W4Weights] = None) -> W4Weights:
+                   out: Optional[W4Weights] = None, stream=None) -> W4Weights:
     """bf16 matrices [.., N, K] to 4 bits (int4: group 128 unless given; fp4:
     group 32).  K is a multiple of 128."""
     if fmt not in _W4_FMT:
@@ -105,116 +124,118 @@ def ep_quantize_w4(w: torch.Tensor, fmt: str = "int4", group: Optional[int] = No
     _gpu(w, "w", _BF16)
     if w.dim() < 1:
         raise ValueError("w must be [.., N, K]")
+    index = w.get_device()
+    if _elsewhere(index, stream):
+        return _there(ep_quantize_w4, index, stream, w, fmt, group, out=out)
     group = int(group) if group is not None else (32 if fmt == "fp4" else 128)
     K = w.shape[-1]
     if group < 1 or K < 1 or K % 128:
         raise ValueError("K must be a multiple of 128 and group positive")
     qs, ss = (*w.shape[:-1], K // 2), (*w.shape[:-1], K // group)
     if out is None:
-        out = W4Weights(torch.empty(qs, dtype=_U8, device=w.device),
-                        torch.empty(ss, dtype=_W4_SCALE[fmt], device=w.device), fmt, group)
+        out = W4Weights(w.new_empty(qs, dtype=_U8), w.new_empty(ss, dtype=_W4_SCALE[fmt]), fmt,
+                        group)
     if out.fmt != fmt or int(out.group) != group:
         raise ValueError("out has another format")
-    _on(out.q, "out.q", _U8, qs, w.device)
-    _on(out.scale, "out.scale", _W4_SCALE[fmt], ss, w.device)
-    st = lib().ep_quantize_w4(_vp(w), w.numel() // K, K, _W4_FMT[fmt], group, _vp(out.q),
-                              _vp(out.scale), _stream(None))
+    _on(out.q, "out.q", _U8, qs, index)
+    _on(out.scale, "out.scale", _W4_SCALE[fmt], ss, index)
+    st = lib().ep_quantize_w4(w.data_ptr(), w.numel() // K, K, _W4_FMT[fmt], group,
+                              out.q.data_ptr(), out.scale.data_ptr(), _raw_stream(index))
     check(st, "ep_quantize_w4")
     return out
 
 
-@_on_device
 def ep_expert_matvec(x: torch.Tensor, weights: Weights, row_expert: Optional[torch.Tensor] = None,
-                     *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                     *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y [R, N] bf16 with y[r] = W[row_expert[r]] x[r], for up to 1024 rows x
     [R, K] bf16 and matrices [E, N, K] (bf16 or W4Weights).  ``row_expert``
     [R] int32 may be left out for one matrix.  Rows whose id lies outside
-    [0, E) are left as they are in ``out``; a result allocated here has zeros
-    there."""
-    _gpu(x, "x", _BF16, 2)
+    [0, E) get zeros."""
+    index = _first(x, "x", _BF16, 2)
+    if _elsewhere(index, stream):
+        return _there(ep_expert_matvec, index, stream, x, weights, row_expert, out=out)
     R, K = x.shape
-    dev = x.device
-    E, N, wk, fmt, group, q, scale = _weights(weights, "weights", dev)
+    E, N, wk, fmt, group, q, scale = _weights(weights, "weights", index)
     if wk != K:
         raise ValueError(f"weights have {wk} channels, x has {K}")
     if row_expert is not None:
-        _on(row_expert, "row_expert", _I32, (R,), dev)
+        _on(row_expert, "row_expert", _I32, (R,), index)
     elif E != 1:
         raise ValueError("row_expert is needed for more than one expert")
     if out is None:
-        out = (torch.empty if row_expert is None else torch.zeros)((R, N), dtype=_BF16, device=dev)
+        out = x.new_empty((R, N))
     else:
-        _on(out, "out", _BF16, (R, N), dev)
-    st = lib().ep_expert_matvec(_vp(x), _vp(row_expert), R, E, N, K, fmt, group, _vp(q),
-                                _vp(scale), _vp(out), _stream(None))
-    check(st, "ep_expert_matvec")
+        _on(out, "out", _BF16, (R, N), index)
+    st = lib().ep_expert_matvec(x.data_ptr(), _ptr(row_expert), R, E, N, K, fmt, group, q, scale,
+                                out.data_ptr(), _raw_stream(index))
+    if st != EP_OK:
+        check(st, "ep_expert_matvec")
     return out
 
 
-def ep_moe_tokens_workspace_bytes(num_tokens: int, num_topk: int, inner: int) -> int:
-    return int(lib().ep_moe_tokens_workspace_bytes(int(num_tokens), int(num_topk), int(inner)))
+@functools.lru_cache(maxsize=1024)
+def ep_moe_tokens_workspace_bytes(num_tokens: int, num_topk: int, hidden: int,
+                                  inner: int) -> int:
+    return int(lib().ep_moe_tokens_workspace_bytes(int(num_tokens), int(num_topk), int(hidden),
+                                                   int(inner)))
 
 
-@_on_device
 def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
                   w13: Weights, w2: Weights, first_expert: int = 0, *, bias=None,
-                  out: Optional[torch.Tensor] = None,
-                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
     """out [T, H] bf16 of a whole expert layer for up to 128 tokens (T*K up to
-    1024), in two launches: out[t] = sum over the slots whose expert e =
-    topk_idx[t, k] - first_expert is one of the E here of topk_weights[t, k] *
-    W2[e] (silu(gate) * up), the gate and up rows being W13[e] x[t].  ``w13``
-    [E, 2I, H] (the gate rows, then the up rows) and ``w2`` [E, H, I] are bf16
-    or W4Weights; ``bias`` is a [T, H] bf16 tensor or a pair, added in fp32
-    before the one rounding, as in ep_combine.
+    1024), in two launches (three for more than four tokens): out[t] = sum over
+    the slots whose expert e = topk_idx[t, k] - first_expert is one of the E
+    here of topk_weights[t, k] * W2[e] (silu(gate) * up), the gate and up rows
+    being W13[e] x[t].  ``w13`` [E, 2I, H] (the gate rows, then the up rows) and
+    ``w2`` [E, H, I] are bf16 or W4Weights; ``bias`` is a [T, H] bf16 tensor or
+    a pair, added in fp32 before the one rounding, as in ep_combine.
 
     Without ``workspace`` (uint8, ep_moe_tokens_workspace_bytes of it) each
     call takes its own from PyTorch's allocator, so calls on several streams
     and captured graphs never share one."""
-    _gpu(x, "x", _BF16, 2)
+    index = _first(x, "x", _BF16, 2)
+    if _elsewhere(index, stream):
+        return _there(ep_moe_tokens, index, stream, x, topk_idx, topk_weights, w13, w2,
+                      first_expert, bias=bias, out=out, workspace=workspace)
     T, H = x.shape
-    dev = x.device
-    _gpu(topk_idx, "topk_idx", _I64, 2)
+    _first(topk_idx, "topk_idx", _I64, 2)
     K = topk_idx.shape[1]
-    _on(topk_idx, "topk_idx", _I64, (T, K), dev)
-    _on(topk_weights, "topk_weights", _F32, (T, K), dev)
-    E, N13, K13, fmt13, group13, q13, scale13 = _weights(w13, "w13", dev)
-    E2, N2, I, fmt2, group2, q2, scale2 = _weights(w2, "w2", dev)
+    _on(topk_idx, "topk_idx", _I64, (T, K), index)
+    _on(topk_weights, "topk_weights", _F32, (T, K), index)
+    E, N13, K13, fmt13, group13, q13, scale13 = _weights(w13, "w13", index)
+    E2, N2, I, fmt2, group2, q2, scale2 = _weights(w2, "w2", index)
     if E2 != E or N2 != H or K13 != H or N13 != 2 * I:
         raise ValueError(f"w13 must be [E, 2I, {H}] and w2 [E, {H}, I], got "
                          f"[{E}, {N13}, {K13}] and [{E2}, {N2}, {I}]")
-    biases = () if bias is None else (tuple(bias) if isinstance(bias, (tuple, list)) else (bias,))
-    if len(biases) > 2:
-        raise ValueError("bias is one [T, H] tensor or a pair")
-    for i, b in enumerate(biases):
-        _on(b, f"bias[{i}]", _BF16, (T, H), dev)
+    b0 = b1 = None
+    if bias is not None:
+        pair = tuple(bias) if isinstance(bias, (tuple, list)) else (bias,)
+        if len(pair) > 2:
+            raise ValueError("bias is one [T, H] tensor or a pair")
+        ptrs = [_on(b, f"bias[{i}]", _BF16, (T, H), index).data_ptr() for i, b in enumerate(pair)]
+        b0, b1 = (ptrs + [None, None])[:2]
     if out is None:
-        out = torch.empty((T, H), dtype=_BF16, device=dev)
+        out = x.new_empty((T, H))
     else:
-        _on(out, "out", _BF16, (T, H), dev)
+        _on(out, "out", _BF16, (T, H), index)
     if workspace is None:
-        workspace = torch.empty(ep_moe_tokens_workspace_bytes(T, K, I), dtype=_U8, device=dev)
-    else:
-        _gpu(workspace, "workspace", _U8)
-        if workspace.device != dev:
-            raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+        workspace = x.new_empty(ep_moe_tokens_workspace_bytes(T, K, H, I), dtype=_U8)
+    elif _first(workspace, "workspace", _U8, 1) != index:
+        raise ValueError(f"workspace is on {workspace.device}, not on cuda:{index}")
     st = lib().ep_moe_tokens(
-        _vp(x), _vp(topk_idx), _vp(topk_weights), T, K, H, I, int(first_expert), E, fmt13, group13,
-        _vp(q13), _vp(scale13), fmt2, group2, _vp(q2), _vp(scale2),
-        _vp(biases[0] if biases else None), _vp(biases[1] if len(biases) > 1 else None), _vp(out),
-        _vp(workspace), workspace.numel(), _stream(None))
-    check(st, "ep_moe_tokens")
+        x.data_ptr(), topk_idx.data_ptr(), topk_weights.data_ptr(), T, K, H, I, int(first_expert),
+        E, fmt13, group13, q13, scale13, fmt2, group2, q2, scale2, b0, b1, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(index))
+    if st != EP_OK:
+        check(st, "ep_moe_tokens")
     return out
 
 
-def _row_count(t: Optional[torch.Tensor], dev):
-    return None if t is None else _on(t, "row_count", _I32, (1,), dev)
-
-
-@_on_device
 def ep_swiglu_fp8(gate_up: torch.Tensor, *, row_count: Optional[torch.Tensor] = None,
                   out: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
-                  scale: Optional[torch.Tensor] = None
+                  scale: Optional[torch.Tensor] = None, stream=None
                   ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(h [R, I] bf16 = silu(gate) * up, q [R, 2I] float8_e4m3fn, scale
     [R, 2I/128] float32) of gate_up [R, 2I] bf16 (I gate channels, then I up
@@ -222,61 +243,66 @@ def ep_swiglu_fp8(gate_up: torch.Tensor, *, row_count: Optional[torch.Tensor] = 
     ep_swiglu_fp8_backward takes in place of gate_up and h.  Rows from
     ``row_count`` ([1] int32 on the device, e.g. ``expert_offsets[-1:]``) on
     are left as they are."""
-    _gpu(gate_up, "gate_up", _BF16, 2)
+    index = _first(gate_up, "gate_up", _BF16, 2)
+    if _elsewhere(index, stream):
+        return _there(ep_swiglu_fp8, index, stream, gate_up, row_count=row_count, out=out, q=q,
+                      scale=scale)
     R, two = gate_up.shape
     if two % 256 or two == 0:
         raise ValueError("gate_up must be [R, 2I] with I a multiple of 128")
-    I, dev = two // 2, gate_up.device
-    count = _row_count(row_count, dev)
-    h = torch.empty((R, I), dtype=_BF16, device=dev) if out is None else \
-        _on(out, "out", _BF16, (R, I), dev)
-    q = torch.empty((R, two), dtype=_FP8, device=dev) if q is None else \
-        _on(q, "q", _FP8, (R, two), dev)
-    scale = torch.empty((R, two // 128), dtype=_F32, device=dev) if scale is None else \
-        _on(scale, "scale", _F32, (R, two // 128), dev)
-    st = lib().ep_swiglu_fp8(_vp(gate_up), R, I, _vp(count), _vp(h), _vp(q), _vp(scale),
-                             _stream(None))
-    check(st, "ep_swiglu_fp8")
+    I = two // 2
+    if row_count is not None:
+        _on(row_count, "row_count", _I32, (1,), index)
+    h = gate_up.new_empty((R, I)) if out is None else _on(out, "out", _BF16, (R, I), index)
+    q = gate_up.new_empty((R, two), dtype=_FP8) if q is None else \
+        _on(q, "q", _FP8, (R, two), index)
+    scale = gate_up.new_empty((R, two // 128), dtype=_F32) if scale is None else \
+        _on(scale, "scale", _F32, (R, two // 128), index)
+    st = lib().ep_swiglu_fp8(gate_up.data_ptr(), R, I, _ptr(row_count), h.data_ptr(), q.data_ptr(),
+                             scale.data_ptr(), _raw_stream(index))
+    if st != EP_OK:
+        check(st, "ep_swiglu_fp8")
     return h, q, scale
 
 
-@_on_device
 def ep_swiglu_fp8_backward(dh: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, *,
                            row_count: Optional[torch.Tensor] = None, recompute: bool = True,
-                           out: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None
-                           ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                           out: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                           stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """(d_gate_up [R, 2I] bf16, h [R, I] bf16) from dh [R, I] bf16 and the
     checkpoint of ep_swiglu_fp8: the gradient of silu(gate) * up at the values
     the checkpoint stands for, and that product itself (what the second
     product's weight gradient takes), None without ``recompute``."""
-    _gpu(dh, "dh", _BF16, 2)
+    index = _first(dh, "dh", _BF16, 2)
+    if _elsewhere(index, stream):
+        return _there(ep_swiglu_fp8_backward, index, stream, dh, q, scale, row_count=row_count,
+                      recompute=recompute, out=out, h=h)
     R, I = dh.shape
     if I % 128 or I == 0:
         raise ValueError("dh must be [R, I] with I a multiple of 128")
-    dev = dh.device
-    _on(q, "q", _FP8, (R, 2 * I), dev)
-    _on(scale, "scale", _F32, (R, I // 64), dev)
-    count = _row_count(row_count, dev)
-    d = torch.empty((R, 2 * I), dtype=_BF16, device=dev) if out is None else \
-        _on(out, "out", _BF16, (R, 2 * I), dev)
+    _on(q, "q", _FP8, (R, 2 * I), index)
+    _on(scale, "scale", _F32, (R, I // 64), index)
+    if row_count is not None:
+        _on(row_count, "row_count", _I32, (1,), index)
+    d = dh.new_empty((R, 2 * I)) if out is None else _on(out, "out", _BF16, (R, 2 * I), index)
     if not recompute:
         if h is not None:
             raise ValueError("h is an output of recompute=True")
     elif h is None:
-        h = torch.empty((R, I), dtype=_BF16, device=dev)
+        h = dh.new_empty((R, I))
     else:
-        _on(h, "h", _BF16, (R, I), dev)
-    st = lib().ep_swiglu_fp8_backward(_vp(dh), _vp(q), _vp(scale), R, I, _vp(count), _vp(d),
-                                      _vp(h), _stream(None))
-    check(st, "ep_swiglu_fp8_backward")
+        _on(h, "h", _BF16, (R, I), index)
+    st = lib().ep_swiglu_fp8_backward(dh.data_ptr(), q.data_ptr(), scale.data_ptr(), R, I,
+                                      _ptr(row_count), d.data_ptr(), _ptr(h), _raw_stream(index))
+    if st != EP_OK:
+        check(st, "ep_swiglu_fp8_backward")
     return d, h
 
 
-@_on_device
 def ep_combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], token_row: torch.Tensor,
                         topk_weights: Optional[torch.Tensor], *, weight_grad: Optional[bool] = None,
                         num_rows: Optional[int] = None, dy: Optional[torch.Tensor] = None,
-                        dw: Optional[torch.Tensor] = None
+                        dw: Optional[torch.Tensor] = None, stream=None
                         ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Gradient of ep_combine: (dy, shaped as y, bf16; dw [T, K] float32).
     dy[r] = (the sum of the weights of the slots that name row r) * dout[t],
@@ -285,37 +311,37 @@ def ep_combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], token_row
     it may then be None, with ``num_rows`` or ``dy`` giving the rows.  Rows no
     slot names are left as they are in ``dy``; a result allocated here has
     zeros there.  The gradient of a combine's bias is dout itself."""
-    _gpu(dout, "dout", _BF16, 2)
+    index = _first(dout, "dout", _BF16, 2)
+    if _elsewhere(index, stream):
+        return _there(ep_combine_backward, index, stream, dout, y, token_row, topk_weights,
+                      weight_grad=weight_grad, num_rows=num_rows, dy=dy, dw=dw)
     T, H = dout.shape
-    dev = dout.device
-    _gpu(token_row, "token_row", _I32, 2)
+    _first(token_row, "token_row", _I32, 2)
     K = token_row.shape[1]
-    _on(token_row, "token_row", _I32, (T, K), dev)
+    _on(token_row, "token_row", _I32, (T, K), index)
     if topk_weights is not None:
-        _on(topk_weights, "topk_weights", _F32, (T, K), dev)
+        _on(topk_weights, "topk_weights", _F32, (T, K), index)
     if weight_grad is None:
         weight_grad = topk_weights is not None
     elif weight_grad and topk_weights is None:
         raise ValueError("weight_grad needs topk_weights")
-    if weight_grad and y is None:
-        raise ValueError("the weights' gradient needs y")
     if y is not None:
-        _gpu(y, "y", _BF16)
-        if y.dim() < 2 or y.shape[-1] != H or y.device != dev:
-            raise ValueError(f"y must be [.., {H}] on {dev}")
         shape = tuple(y.shape)
+        _on(y, "y", _BF16, shape, index)
+    elif weight_grad:
+        raise ValueError("the weights' gradient needs y")
     elif dy is not None:
         shape = tuple(dy.shape)
     elif num_rows is not None:
         shape = (int(num_rows), H)
     else:
         raise ValueError("without y, num_rows or dy gives the rows")
+    if len(shape) < 2 or shape[-1] != H:
+        raise ValueError(f"y and dy must be [.., {H}], got {shape}")
     if dy is None:
-        dy = torch.zeros(shape, dtype=_BF16, device=dev)
-    elif len(shape) < 2 or shape[-1] != H:
-        raise ValueError(f"dy must be [.., {H}]")
+        dy = dout.new_zeros(shape)
     else:
-        _on(dy, "dy", _BF16, shape, dev)
+        _on(dy, "dy", _BF16, shape, index)
     rows = dy.numel() // H if H else 0
     if num_rows is not None and int(num_rows) != rows:
         raise ValueError(f"num_rows is {num_rows}, the buffers have {rows}")
@@ -323,11 +349,12 @@ def ep_combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], token_row
         if dw is not None:
             raise ValueError("dw is an output of weight_grad=True")
     elif dw is None:
-        dw = torch.empty((T, K), dtype=_F32, device=dev)
+        dw = dout.new_empty((T, K), dtype=_F32)
     else:
-        _on(dw, "dw", _F32, (T, K), dev)
-    st = lib().ep_combine_backward(_vp(dout), _vp(y) if weight_grad else None, rows,
-                                   _vp(token_row), _vp(topk_weights), T, K, H, _vp(dy), _vp(dw),
-                                   _stream(None))
-    check(st, "ep_combine_backward")
+        _on(dw, "dw", _F32, (T, K), index)
+    st = lib().ep_combine_backward(dout.data_ptr(), y.data_ptr() if weight_grad else None, rows,
+                                   token_row.data_ptr(), _ptr(topk_weights), T, K, H,
+                                   dy.data_ptr(), _ptr(dw), _raw_stream(index))
+    if st != EP_OK:
+        check(st, "ep_combine_backward")
     return dy, dw

@@ -84,7 +84,8 @@ int main(int argc, char** argv) {
                                  pick(kI64), pick(kI32), pick(kI32), ptr(), p<float>(), nullptr);
         break;
       default: {
-        volatile size_t s = ep_moe_tokens_workspace_bytes(pick(kI64), pick(kI32), pick(kI32));
+        volatile size_t s = ep_moe_tokens_workspace_bytes(pick(kI64), pick(kI32), pick(kI32),
+                                                          pick(kI32));
         (void)s;
         continue;
       }

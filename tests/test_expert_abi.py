@@ -78,10 +78,11 @@ def test_layer_refusals():
         (dict(s2=None), BAD), (dict(ws=None), WS), (dict(ws=A16), WS), (dict(bytes=1000), WS),
         (dict(T=0, x=None, idx=None, tw=None, out=None), 0)])
     size = _lib.lib().ep_moe_tokens_workspace_bytes
-    assert size(4, 2, 128) == size(0, 2, 128) + 8 * 128 * 4
-    assert call(_lib.lib().ep_moe_tokens, args, bytes=size(4, 2, 128) - 1) == WS
-    for bad in ((-1, 2, 128), (4, 0, 128), (4, 2, 0), (129, 1, 128), (128, 9, 128), (4, 17, 128),
-                (4, 2, 65537), (1 << 62, 2, 128)):
+    assert size(4, 2, 256, 128) == size(0, 2, 256, 128) + 8 * 128 * 4
+    assert call(_lib.lib().ep_moe_tokens, args, bytes=size(4, 2, 256, 128) - 1) == WS
+    for bad in ((-1, 2, 256, 128), (4, 0, 256, 128), (4, 2, 0, 128), (4, 2, 256, 0),
+                (129, 1, 256, 128), (128, 9, 256, 128), (4, 17, 256, 128), (4, 2, 256, 65537),
+                (4, 2, 65537, 128), (1 << 62, 2, 256, 128)):
         assert size(*bad) == 0
 
 

@@ -24,7 +24,7 @@ def dev_weights(t, fmt, group):
 
 # (rows, experts, N, K): one of everything; odd tiles; row counts around the
 # 16- and 32-row tiles; K around the 128-channel block (bf16 also between)
-SHAPES = [(1, 1, 8, 128), (1, 1, 64, 1024), (3, 2, 24, 256), (16, 1, 72, 384), (17, 1, 40, 128),
+SHAPES = [(1, 1, 8, 128), (1, 1, 64, 1024), (2, 1, 136, 2176), (4, 3, 40, 640), (3, 2, 24, 256), (16, 1, 72, 384), (17, 1, 40, 128),
           (33, 3, 16, 640), (70, 2, 136, 256), (5, 40, 48, 128), (200, 7, 56, 256)]
 
 
@@ -49,35 +49,37 @@ def test_matvec_bf16_channel_tails(K):
     rng = np.random.default_rng(K)
     t, v, mag = make_weights(rng, "bf16", 0, 2, 40, K)
     # what lies behind a row must not be multiplied in: the next row is not finite
-    x = bf16(rng.standard_normal((4, K)))
-    x[2] = float("inf")
-    ids = np.array([0, 1, 1, 0], np.int32)
-    y = ep.ep_expert_matvec(x.to(DEV), t[0].to(DEV), torch.from_numpy(ids).to(DEV))
-    keep = [0, 1, 3]
-    ref, tol = matvec_ref(f64(x)[keep], ids[keep], v, mag)
-    check(y[keep], ref, tol)
+    for R in (4, 5):
+        x = bf16(rng.standard_normal((R, K)))
+        x[2] = float("inf")
+        ids = np.array([0, 1, 1, 0, 1], np.int32)[:R]
+        y = ep.ep_expert_matvec(x.to(DEV), t[0].to(DEV), torch.from_numpy(ids).to(DEV))
+        keep = [r for r in range(R) if r != 2]
+        ref, tol = matvec_ref(f64(x)[keep], ids[keep], v, mag)
+        check(y[keep], ref, tol)
 
 
+@pytest.mark.parametrize("R", [3, 21])
 @pytest.mark.parametrize("fmt,group", FORMATS)
-def test_rows_without_an_expert_are_left_alone(fmt, group):
+def test_rows_without_an_expert_get_zeros(fmt, group, R):
     rng = np.random.default_rng(5)
-    E, N, K, R = 3, 40, 256, 21
+    E, N, K = 3, 40, 256
     t, v, mag = make_weights(rng, fmt, group, E, N, K)
     x = bf16(rng.standard_normal((R, K)))
     ids = rng.integers(0, E, R).astype(np.int32)
-    out = [2, 3, 11, 20]
-    ids[out] = [-1, E, -2 ** 31, 2 ** 31 - 1]
+    out = [1, 2] if R == 3 else [2, 3, 11, 20]
+    ids[out] = [-1, E, -2 ** 31, 2 ** 31 - 1][:len(out)]
     x[out] = float("nan")
     buf = torch.full((R + 2, N), 7.0, dtype=torch.bfloat16, device=DEV)
     y = ep.ep_expert_matvec(x.to(DEV), dev_weights(t, fmt, group), torch.from_numpy(ids).to(DEV),
                             out=buf[:R])
-    assert (buf[R:] == 7).all() and (buf[out] == 7).all()
+    assert (buf[R:] == 7).all() and (buf[out].view(torch.int16) == 0).all()
     ref, tol = matvec_ref(f64(x), ids, v, mag)
     keep = [r for r in range(R) if r not in out]
     check(y[keep], ref[keep], tol[keep])
     none = torch.full((R,), -1, dtype=torch.int32, device=DEV)
-    z = ep.ep_expert_matvec(x.to(DEV), dev_weights(t, fmt, group), none)
-    assert (z == 0).all()
+    z = ep.ep_expert_matvec(x.to(DEV), dev_weights(t, fmt, group), none, out=buf[1:R + 1])
+    assert (z.view(torch.int16) == 0).all() and (buf[R + 1:] == 7).all()
 
 
 @pytest.mark.parametrize("fmt,group", FORMATS)
@@ -150,7 +152,7 @@ def test_int4_activations_up_to_their_limit():
 
 LAYERS = [  # T, K, E here, experts in all, first, H, I
     (1, 1, 1, 1, 0, 128, 128), (1, 8, 32, 32, 0, 256, 128), (3, 2, 8, 8, 0, 512, 256),
-    (5, 3, 4, 64, 20, 256, 384), (17, 2, 3, 3, 0, 128, 640), (64, 16, 20, 40, 10, 128, 128),
+    (4, 16, 40, 64, 7, 384, 640), (2, 3, 4, 4, 0, 1152, 128), (5, 3, 4, 64, 20, 256, 384), (17, 2, 3, 3, 0, 128, 640), (64, 16, 20, 40, 10, 128, 128),
     (128, 8, 16, 16, 0, 256, 128), (40, 1, 1, 2, 1, 384, 256)]
 
 
@@ -195,18 +197,19 @@ def test_layer_bf16_tails_biases_and_mixed_formats(H, I):
         check(out, ref, tol, "mixed")
 
 
-def test_layer_ids_of_every_kind():
+@pytest.mark.parametrize("T", [4, 64])
+def test_layer_ids_of_every_kind(T):
     """Ids far outside, one expert named by every slot (more rows than one
     tile of any variant), the same expert twice in a token, nothing routed."""
     rng = np.random.default_rng(11)
-    T, K, E, H, I = 64, 16, 4, 128, 128
+    K, E, H, I = 16, 4, 128, 128
     t13, v13, m13 = make_weights(rng, "fp4", 32, E, 2 * I, H)
     t2, v2, m2 = make_weights(rng, "fp4", 32, E, H, I)
     x = bf16(rng.standard_normal((T, H)))
     w = rng.random((T, K)).astype(np.float32)
     odd = np.full((T, K), 2 ** 62, np.int64)
     odd[::2] = -2 ** 63
-    odd[1, 3], odd[2, 15], odd[63, 0] = 1000, 1003, 1004
+    odd[1, 3], odd[2, 15], odd[-1, 0] = 1000, 1003, 1004
     twice = rng.integers(1000, 1000 + E, (T, K)).astype(np.int64)
     twice[:, 1] = twice[:, 0]
     for name, idx in (("odd", odd), ("one", np.full((T, K), 1002, np.int64)), ("twice", twice),
@@ -240,15 +243,16 @@ def test_layer_skips_what_it_does_not_name():
     check(out, ref, tol)
 
 
-def test_layer_gives_the_same_bits_again_and_keeps_to_its_buffers():
+@pytest.mark.parametrize("tokens", [3, 9, 50, 128])
+def test_layer_gives_the_same_bits_again_and_keeps_to_its_buffers(tokens):
     rng = np.random.default_rng(13)
-    T, K, E, H, I = 50, 8, 16, 256, 256
+    T, K, E, H, I = tokens, 8, 16, 256, 256
     t13, _, _ = make_weights(rng, "int4", 128, E, 2 * I, H)
     t2, _, _ = make_weights(rng, "int4", 128, E, H, I)
     x = bf16(rng.standard_normal((T, H))).to(DEV)
     idx, w = (torch.from_numpy(a).to(DEV) for a in topk(rng, T, K, E))
     w13, w2 = dev_weights(t13, "int4", 128), dev_weights(t2, "int4", 128)
-    n = ep.ep_moe_tokens_workspace_bytes(T, K, I)
+    n = ep.ep_moe_tokens_workspace_bytes(T, K, H, I)
     ws = torch.full((n + 256,), 0xA5, dtype=torch.uint8, device=DEV)
     buf = torch.full((T + 2, H), 7.0, dtype=torch.bfloat16, device=DEV)
     first = ep.ep_moe_tokens(x, idx, w, w13, w2, out=buf[1:T + 1], workspace=ws[:n]).clone()
