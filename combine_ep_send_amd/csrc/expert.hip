@@ -228,93 +228,101 @@ __device__ __forceinline__ void exchange_halves(u32x4& a, u32x4& b) {
   }
 }
 
-// A stage's products into acc: MT tiles of 16 rows x against NT tiles of 16
-// weight rows.  A row x is the sum of XP bf16 rows.  x(mt, p, q, j): the
-// fragment of row tile mt, part p, for product j of vector q (bf16: q alone),
-// as order_x leaves it; use(mt): whether the tile has rows at all.
-template <int KIND, int NT, int NV, int MT, int XP, typename X, typename Use>
-__device__ __forceinline__ void stage_products(Stage<KIND, NT, NV>& st, X x, Use use,
-                                               f32x4 (&acc)[MT][NT]) {
+// The scale words of a stage's vectors, one set for every lane.
+template <int KIND, int NT, int NV>
+struct Scales {
   uint32_t s0[NT][NV], s1[NT][NV];
+};
+
+// A stage as loaded, put in order.
+template <int KIND, int NT, int NV>
+__device__ __forceinline__ void open_stage(Stage<KIND, NT, NV>& st, Scales<KIND, NT, NV>& sc) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int q = 0; q < NV; q += 2) exchange_halves(st.v[nt][q], st.v[nt][q + 1]);
-    if constexpr (KIND != kWBf16) spread_groups<NV>(st.s[nt][0], s0[nt]);
-    if constexpr (KIND == kWInt4G32) spread_groups<NV>(st.s[nt][1], s1[nt]);
+    if constexpr (KIND != kWBf16) spread_groups<NV>(st.s[nt][0], sc.s0[nt]);
+    if constexpr (KIND == kWInt4G32) spread_groups<NV>(st.s[nt][1], sc.s1[nt]);
   }
+}
+
+// Vector q's products into acc: MT tiles of 16 rows x against NT tiles of 16
+// weight rows.  A row x is the sum of XP bf16 rows.  x(mt, p, j): the fragment
+// of row tile mt, part p, for product j of the vector (bf16: the only one), as
+// order_x leaves it; use(mt): whether the tile has rows at all.
+template <int KIND, int NT, int NV, int MT, int XP, typename X, typename Use>
+__device__ __forceinline__ void vector_products(const Stage<KIND, NT, NV>& st,
+                                                const Scales<KIND, NT, NV>& scales, int q, X x,
+                                                Use use, f32x4 (&acc)[MT][NT]) {
+  if constexpr (KIND == kWBf16) {
 #pragma unroll
-  for (int q = 0; q < NV; ++q) {
-    if constexpr (KIND == kWBf16) {
+    for (int mt = 0; mt < MT; ++mt) {
+      if (!use(mt)) continue;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (!use(mt)) continue;
+      for (int p = 0; p < XP; ++p) {
+        const u32x4 a = x(mt, p, 0);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = mfma(a, st.v[nt][q], acc[mt][nt]);
+      }
+    }
+  } else if constexpr (KIND == kWFp4) {
+    u32x4 b[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t byte = scales.s0[nt][q] >> ((lane_id() >> 4) * 8);   // lane group g: byte g
+      const float sc = __uint_as_float((byte << 23) & 0x7F800000u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[nt][j] = decode_fp4(st.v[nt][q][j], sc);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      if (!use(mt)) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int p = 0; p < XP; ++p) {
-          const u32x4 a = x(mt, p, q, 0);
+          const u32x4 a = x(mt, p, j);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = mfma(a, st.v[nt][q], acc[mt][nt]);
+          for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = mfma(a, b[nt][j], acc[mt][nt]);
         }
-      }
-    } else if constexpr (KIND == kWFp4) {
-      u32x4 b[NT][4];
+    }
+  } else {
+    constexpr int Q = KIND == kWInt4G128 ? 1 : KIND == kWInt4G64 ? 2 : 4;   // groups a vector
+    constexpr int J = 4 / Q;                                                // products a group
+    const u32x4 minus = {kMinus24, kMinus24, kMinus24, kMinus24};
+    u32x4 b[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t byte = s0[nt][q] >> ((lane_id() >> 4) * 8);   // lane group g: byte g
-        const float sc = __uint_as_float((byte << 23) & 0x7F800000u);
+    for (int nt = 0; nt < NT; ++nt) {
+      const u32x4 v = kSplit<KIND> ? st.v[nt][q] : transpose_groups(st.v[nt][q]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[nt][j] = decode_fp4(st.v[nt][q][j], sc);
-      }
+      for (int j = 0; j < 4; ++j) b[nt][j] = decode_int4(v[j]);
+    }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (!use(mt)) continue;
+    for (int mt = 0; mt < MT; ++mt) {
+      if (!use(mt)) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+      for (int i = 0; i < Q; ++i) {
+        f32x4 base = {0.f, 0.f, 0.f, 0.f};
+        u32x4 a[J][XP];
+#pragma unroll
+        for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int p = 0; p < XP; ++p) {
-            const u32x4 a = x(mt, p, q, j);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[mt][nt] = mfma(a, b[nt][j], acc[mt][nt]);
+            a[j][p] = x(mt, p, i * J + j);
+            base = mfma(a[j][p], minus, base);
           }
-      }
-    } else {
-      constexpr int Q = KIND == kWInt4G128 ? 1 : KIND == kWInt4G64 ? 2 : 4;   // groups a vector
-      constexpr int J = 4 / Q;                                                // products a group
-      const u32x4 minus = {kMinus24, kMinus24, kMinus24, kMinus24};
-      u32x4 b[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const u32x4 v = kSplit<KIND> ? st.v[nt][q] : transpose_groups(st.v[nt][q]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) b[nt][j] = decode_int4(v[j]);
-      }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        if (!use(mt)) continue;
-#pragma unroll
-        for (int i = 0; i < Q; ++i) {
-          f32x4 base = {0.f, 0.f, 0.f, 0.f};
-          u32x4 a[J][XP];
+        for (int nt = 0; nt < NT; ++nt) {
+          f32x4 part = base;
 #pragma unroll
           for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int p = 0; p < XP; ++p) {
-              a[j][p] = x(mt, p, q, i * J + j);
-              base = mfma(a[j][p], minus, base);
-            }
+            for (int p = 0; p < XP; ++p) part = mfma(a[j][p], b[nt][i * J + j], part);
+          const uint32_t sw = i < 2 ? scales.s0[nt][q] : scales.s1[nt][q];
+          const float sc = Q > 1 && (i & 1) ? bf16_hi(sw) : bf16_lo(sw);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            f32x4 part = base;
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-              for (int p = 0; p < XP; ++p) part = mfma(a[j][p], b[nt][i * J + j], part);
-            const uint32_t sw = i < 2 ? s0[nt][q] : s1[nt][q];
-            const float sc = Q > 1 && (i & 1) ? bf16_hi(sw) : bf16_lo(sw);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              acc[mt][nt][k] = __builtin_fmaf(sc, part[k], acc[mt][nt][k]);
-          }
+          for (int k = 0; k < 4; ++k)
+            acc[mt][nt][k] = __builtin_fmaf(sc, part[k], acc[mt][nt][k]);
         }
       }
     }
@@ -377,15 +385,19 @@ __device__ __forceinline__ void own_tile(rsrc_t xr, uint32_t xoff, int plane, u3
           xs[((b * XP + p) * kFewRows + (lane >> 4)) * kXPitch<KIND> + (lane & 15)] =
               order_x<KIND>(xb[d][b][p]);
       __builtin_amdgcn_wave_barrier();
-      stage_products<KIND, NT, NV, 1, XP>(
-          w[d],
-          [&](int, int p, int q, int j) {
-            const int g = lane >> 4;
-            const int b = KIND == kWBf16 ? q / 4 : q, i = KIND == kWBf16 ? q % 4 : j;
-            const int piece = kSplit<KIND> ? g * 4 + i : i * 4 + g;
-            return xs[((b * XP + p) * kFewRows + (lane & 3)) * kXPitch<KIND> + piece];
-          },
-          [](int) { return true; }, acc);
+      Scales<KIND, NT, NV> sc;
+      open_stage<KIND, NT, NV>(w[d], sc);
+#pragma unroll
+      for (int q = 0; q < NV; ++q)
+        vector_products<KIND, NT, NV, 1, XP>(
+            w[d], sc, q,
+            [&](int, int p, int j) {
+              const int g = lane >> 4;
+              const int b = KIND == kWBf16 ? q / 4 : q, i = KIND == kWBf16 ? q % 4 : j;
+              const int piece = kSplit<KIND> ? g * 4 + i : i * 4 + g;
+              return xs[((b * XP + p) * kFewRows + (lane & 3)) * kXPitch<KIND> + piece];
+            },
+            [](int) { return true; }, acc);
       __builtin_amdgcn_wave_barrier();
       // kept in this order, so that a stage's wait leaves the later stages'
       // loads in flight
@@ -600,13 +612,13 @@ __device__ __forceinline__ void lds_barrier() {
 // 64*NT weight rows.
 // ---------------------------------------------------------------------------
 template <int KIND, int NT, int NV, int MT, int XP, int OUT, int D>
-__global__ __launch_bounds__(kBlock) void few_wide_kernel(FewArgs a) {
+__global__ __launch_bounds__(kBlock, 2) void few_wide_kernel(FewArgs a) {
   constexpr bool GATED = OUT == kOutGated;
   constexpr int C = GATED ? NT / 2 : NT;               // tiles of output channels a wave
   constexpr int XB = kXBlocks<KIND, NV>;
-  static_assert(D % 2 == 0, "the two buffers of x take turns");
+  static_assert(D * XB % 2 == 0, "the two buffers of x take turns");
   __shared__ SharedPlan sp;
-  __shared__ u32x4 xs[2][MT][XP][XB][4][kWave];
+  __shared__ u32x4 xs[2][MT][XP][4][kWave];
   const int lane = lane_id(), wave = wave_id();
   int e = 0, first = 0, active = 0;
   int m = find_expert<kBlock>(sp, a, blockIdx.y, e, first, active);
@@ -628,12 +640,19 @@ __global__ __launch_bounds__(kBlock) void few_wide_kernel(FewArgs a) {
   const int stages = (a.K + NV * kVecK<KIND> - 1) / (NV * kVecK<KIND>);
   for (int c0 = 0; c0 < m; c0 += 16 * MT) {
     const int left = m - c0;
-    // this wave fetches product `wave` of every 128 channels: the lane's piece
-    const int piece = kSplit<KIND> ? (lane >> 4) * 4 + wave : wave * 4 + (lane >> 4);
+    // This wave fetches rows 4*wave.. of every tile, 256 bytes of four rows a
+    // load.  A fragment is 64 pieces of 16 bytes, g*16 + row for lane group g;
+    // piece c goes into fragment and group (c % 4, c / 4) or the other way
+    // round, and its place among the group's 16 turns by c: writes (one row,
+    // 16 pieces) and reads (one piece, 16 rows) both reach all the banks.
+    const int row = wave * 4 + (lane >> 4), piece = lane & 15;
+    const int frag = kSplit<KIND> ? piece & 3 : piece >> 2;
+    const int group = kSplit<KIND> ? piece >> 2 : piece & 3;
+    const int to = group * 16 + ((row + piece) & 15);
     uint32_t xoff[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int i = c0 + mt * 16 + (lane & 15);
+      const int i = c0 + mt * 16 + row;
       xoff[mt] = i < m ? uint32_t(sp.list[i] / a.top) * uint32_t(a.K * 2 * XP) +
                              uint32_t(piece * 16)
                        : kOob;
@@ -671,24 +690,29 @@ __global__ __launch_bounds__(kBlock) void few_wide_kernel(FewArgs a) {
     for (int st = 0; st < stages; st += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        // D is even, so that d % 2 alternates over the whole loop: a buffer is
-        // written again only after the barrier that follows its last reads
-        const int buf = d & 1;
+        Scales<KIND, NT, NV> sc;
+        open_stage<KIND, NT, NV>(w[d], sc);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int b = 0; b < XB; ++b) {
+          // the buffers alternate over the whole loop (D * XB is even): one is
+          // written again only after the barrier that follows its last reads
+          const int buf = (d * XB + b) & 1;
 #pragma unroll
-          for (int p = 0; p < XP; ++p)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int b = 0; b < XB; ++b)
-              xs[buf][mt][p][b][wave][lane] = order_x<KIND>(xb[d][mt][p][b]);
-        lds_barrier();
-        stage_products<KIND, NT, NV, MT, XP>(
-            w[d],
-            [&](int mt, int p, int q, int j) {
-              return KIND == kWBf16 ? xs[buf][mt][p][q / 4][q % 4][lane]
-                                    : xs[buf][mt][p][q][j][lane];
-            },
-            [&](int mt) { return mt == 0 || mt * 16 < left; }, acc);
+            for (int p = 0; p < XP; ++p) xs[buf][mt][p][frag][to] = order_x<KIND>(xb[d][mt][p][b]);
+          lds_barrier();
+#pragma unroll
+          for (int q = b * (NV / XB); q < (b + 1) * (NV / XB); ++q)
+            vector_products<KIND, NT, NV, MT, XP>(
+                w[d], sc, q,
+                [&](int mt, int p, int j) {
+                  const int f = KIND == kWBf16 ? q % 4 : j, g = lane >> 4;
+                  const int c = kSplit<KIND> ? g * 4 + f : f * 4 + g;
+                  return xs[buf][mt][p][f][g * 16 + ((lane + c) & 15)];
+                },
+                [&](int mt) { return mt == 0 || mt * 16 < left; }, acc);
+        }
         __builtin_amdgcn_sched_barrier(0);             // as in own_tile
         load(d, st + d + D);
         __builtin_amdgcn_sched_barrier(0);
@@ -731,13 +755,14 @@ constexpr int kDownBlock = kDownWaves * kWave;
 constexpr int kDownMaxSplit = 8;
 constexpr int kDownSlots = 64;                         // most slots: kFewRows tokens of 16
 
-template <int KIND, int NV, int D>
+template <int KIND, int NT, int NV, int D>
 __global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a) {
-  extern __shared__ float prod[];                      // [split][slots][16]
+  extern __shared__ float prod[];                      // [split][slots][C]
   __shared__ u32x4 xs[kDownWaves][kXPieces<KIND, NV, 2>];
   __shared__ int16_t expert[kDownSlots], order[kDownSlots], first[kDownSlots], count[kDownSlots];
   __shared__ float weight[kDownSlots];
   __shared__ uint8_t local[kDownSlots];
+  constexpr int C = NT * 16;
   const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
   const int slots = a.T * a.K;
   const int active = a.plan->active;
@@ -762,9 +787,9 @@ __global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a) {
       if (cost < best) best = cost, split = s;
     }
   }
-  const int n0 = blockIdx.x * 16;
-  Rows<1> rows;
-  set_rows<KIND, 1, NV>(rows, a.I, [&](int) { return n0; }, n0, a.H, 1);
+  const int n0 = blockIdx.x * C;
+  Rows<NT> rows;
+  set_rows<KIND, NT, NV>(rows, a.I, [&](int nt) { return n0 + nt * 16; }, n0, a.H, NT);
   const rsrc_t xr = make_rsrc(a.h, int64_t(slots) * a.I * 4);
   for (int u = wave; u < active * split; u += kDownWaves) {
     const int i = u / split, part = u % split;
@@ -777,25 +802,30 @@ __global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a) {
       const int r = c0 + (lane >> 4);
       const uint32_t xoff =
           r < m ? uint32_t(order[f + r]) * uint32_t(a.I * 4) + uint32_t(lane & 15) * 16u : kOob;
-      f32x4 acc[1][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}};
-      own_tile<KIND, 1, NV, 2, D>(xr, xoff, a.I * 2, xs[wave], wr, sr, rows, a.I,
+      f32x4 acc[1][NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[0][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      own_tile<KIND, NT, NV, 2, D>(xr, xoff, a.I * 2, xs[wave], wr, sr, rows, a.I,
                                   part * stages / split, (part + 1) * stages / split, 1, acc);
       if (lane < 16) {
 #pragma unroll
         for (int k = 0; k < kFewRows; ++k)
-          if (c0 + k < m) prod[(part * slots + order[f + c0 + k]) * 16 + lane] = acc[0][0][k];
+          if (c0 + k < m)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              prod[(part * slots + order[f + c0 + k]) * C + nt * 16 + lane] = acc[0][nt][k];
       }
     }
   }
   __syncthreads();
-  if (tid < a.T * 16 && n0 + (tid & 15) < a.H) {
-    const int t = tid >> 4, ch = n0 + (tid & 15);
+  if (tid < a.T * C && n0 + tid % C < a.H) {           // at most kFewRows * C threads
+    const int t = tid / C, ch = n0 + tid % C;
     float sum = 0.f;
     for (int k = 0; k < a.K; ++k) {
       const int s = t * a.K + k;
       if (!local[s]) continue;
       float y = 0.f;
-      for (int p = 0; p < split; ++p) y += prod[(p * slots + s) * 16 + (tid & 15)];
+      for (int p = 0; p < split; ++p) y += prod[(p * slots + s) * C + tid % C];
       sum += weight[s] * y;
     }
     const int64_t o = int64_t(t) * a.H + ch;
@@ -905,40 +935,91 @@ __global__ __launch_bounds__(kBlock) void quantize_w4_kernel(QuantArgs a, int64_
   static_cast<uint32_t*>(a.q)[p] = code;
 }
 
-// Tuning of the launches.
-template <int KIND> constexpr int kThinNV = KIND == kWBf16 ? 4 : 2;
-template <int KIND> constexpr int kThinD = 2;
-constexpr int kThinW = 4;
-template <int KIND> constexpr int kWideNT = 2;
-template <int KIND> constexpr int kWideNV = KIND == kWBf16 ? 4 : 2;
-template <int KIND> constexpr int kWideD = 2;
-constexpr int kWideMT = 2;
-template <int KIND> constexpr int kDownNV = KIND == kWBf16 ? 4 : 2;
-template <int KIND> constexpr int kDownD = 2;
-
 unsigned most_experts(const FewArgs& a) {
   return unsigned(a.slots < a.experts ? a.slots : a.experts);
 }
 
-template <int KIND, int OUT>
-hipError_t wide_variant(const FewArgs& a, hipStream_t s) {
-  constexpr int NT = kWideNT<KIND>;
+// Workgroups of a launch whose workgroups cover `channels` output channels.
+int64_t groups_of(const FewArgs& a, int channels) {
+  return int64_t((a.N + channels - 1) / channels) * most_experts(a);
+}
+
+constexpr int kCus = 256;
+
+template <int KIND, int NT, int MT, int OUT>
+hipError_t launch_wide(const FewArgs& a, hipStream_t s) {
   constexpr int C = (OUT == kOutGated ? NT / 2 : NT) * 16 * kWavesPerBlock;
+  constexpr int NV = KIND == kWBf16 ? 4 : 2;           // 256 bytes of a bf16 row, 128 of a 4-bit one
   constexpr int XP = OUT == kOutF32 ? 2 : 1;
   const dim3 grid(unsigned((a.N + C - 1) / C), most_experts(a));
-  few_wide_kernel<KIND, NT, kWideNV<KIND>, kWideMT, XP, OUT, kWideD<KIND>>
-      <<<grid, kBlock, 0, s>>>(a);
+  few_wide_kernel<KIND, NT, NV, MT, XP, OUT, 2><<<grid, kBlock, 0, s>>>(a);
   return hipGetLastError();
 }
 
+// The wide form's tiles.  Rows: an expert's rows are not known here, so the
+// average over the experts stands for them; 48 rows at a time from 28 on (32
+// rows each of 32 int4 experts of 7168 x 2048: 366 us against 435 with 32 rows
+// at a time, which read half the weights twice; 8 bf16 experts with three rows
+// each, where 25 were possible: 64 against 60), 16 where no more can come or
+// are likely.  Weight rows: two tiles a wave; four for bf16 if that still
+// gives most compute units a workgroup (48 rows, 8 matrices of 7168 x 2048: 41
+// us against 48; 128 workgroups instead of 256 took 30 against 19; 4-bit ones
+// need too many registers: 740 against 435), and one for a matrix too small
+// for half the units (9 rows, 4 fp4 matrices of 1000 x 640: 6.2 against 7.6).
+template <int KIND, int OUT>
+hipError_t wide_variant(const FewArgs& a, hipStream_t s) {
+  constexpr int half = OUT == kOutGated ? 2 : 1;       // a gate and an up tile an output tile
+  const int average = (a.slots + a.experts - 1) / a.experts;
+  const int mt = a.rows <= 16 * (OUT == kOutF32 ? a.per_token : 1) || average <= 12 ? 1
+                 : average < 28 ? 2 : 3;
+  if (mt == 3) return launch_wide<KIND, 2, 3, OUT>(a, s);
+  if constexpr (KIND == kWBf16) {
+    if (groups_of(a, 4 / half * 64) >= kCus * 3 / 4)
+      return mt == 1 ? launch_wide<KIND, 4, 1, OUT>(a, s) : launch_wide<KIND, 4, 2, OUT>(a, s);
+  }
+  if constexpr (OUT == kOutBf16) {
+    if (groups_of(a, 128) < kCus / 2)
+      return mt == 1 ? launch_wide<KIND, 1, 1, OUT>(a, s) : launch_wide<KIND, 1, 2, OUT>(a, s);
+  }
+  return mt == 1 ? launch_wide<KIND, 2, 1, OUT>(a, s) : launch_wide<KIND, 2, 2, OUT>(a, s);
+}
+
+template <int KIND, int OUT, int W>
+hipError_t launch_thin(const FewArgs& a, hipStream_t s) {
+  constexpr int NT = OUT == kOutGated ? 2 : 1;
+  constexpr int NV = KIND == kWBf16 ? 4 : 2;
+  const dim3 grid(unsigned((a.N + 15) / 16), most_experts(a));
+  few_thin_kernel<KIND, NT, NV, W, OUT, 2><<<grid, W * kWave, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// The thin form: four waves a workgroup, or eight where few workgroups have
+// long rows (one row, int4 4096 x 7168, 256 workgroups: 8.0 against 9.4 us;
+// one token through 8 fp4 experts, 1024 workgroups: 33 against 28).
 template <int KIND, int OUT>
 hipError_t thin_variant(const FewArgs& a, hipStream_t s) {
-  constexpr int NT = OUT == kOutGated ? 2 : 1;
-  constexpr int C = (OUT == kOutGated ? NT / 2 : NT) * 16;
-  const dim3 grid(unsigned((a.N + C - 1) / C), most_experts(a));
-  few_thin_kernel<KIND, NT, kThinNV<KIND>, kThinW, OUT, kThinD<KIND>>
-      <<<grid, kThinW * kWave, 0, s>>>(a);
+  if (groups_of(a, 16) <= 2 * kCus && a.K >= 4096) return launch_thin<KIND, OUT, 8>(a, s);
+  return launch_thin<KIND, OUT, 4>(a, s);
+}
+
+// The down products of up to four tokens: 32 channels a workgroup for 4-bit
+// weights if that leaves enough workgroups, else 16 (one token, 8 fp4 experts
+// of 7168 x 2048: 19.9 against 22.5 us; bf16, 512 x 256: 7.3 against 5.8).
+template <int KIND, int NT>
+hipError_t launch_down(const DownArgs& a, hipStream_t s) {
+  constexpr int C = NT * 16;
+  constexpr int NV = KIND == kWBf16 ? 4 : 2;
+  few_down_kernel<KIND, NT, NV, 2>
+      <<<dim3(unsigned((a.H + C - 1) / C)), kDownBlock,
+         size_t(kDownMaxSplit) * size_t(a.T * a.K) * C * 4, s>>>(a);
   return hipGetLastError();
+}
+
+template <int KIND>
+hipError_t down_variant(const DownArgs& a, hipStream_t s) {
+  if constexpr (KIND != kWBf16)
+    if (a.H >= 32 * kCus * 3 / 4) return launch_down<KIND, 2>(a, s);
+  return launch_down<KIND, 1>(a, s);
 }
 
 // Calls fn with the weight kind as a compile-time constant.
@@ -969,11 +1050,7 @@ hipError_t launch_few_rows(const FewArgs& a, bool gated, hipStream_t s) {
 hipError_t launch_few_down(const DownArgs& a, hipStream_t s) {
   if (!few_is_wide(a.T))
     return with_kind(a.w.kind, [&](auto kind) {
-      constexpr int KIND = decltype(kind)::value;
-      few_down_kernel<KIND, kDownNV<KIND>, kDownD<KIND>>
-          <<<dim3(unsigned((a.H + 15) / 16)), kDownBlock,
-             size_t(kDownMaxSplit) * size_t(a.T * a.K) * 64, s>>>(a);
-      return hipGetLastError();
+      return down_variant<decltype(kind)::value>(a, s);
     });
   FewArgs f{};
   f.x = a.h;
@@ -982,6 +1059,7 @@ hipError_t launch_few_down(const DownArgs& a, hipStream_t s) {
   f.slots = a.T * a.K;
   f.top = 1;
   f.rows = f.slots;
+  f.per_token = a.K;
   f.experts = a.experts;
   f.N = a.H;
   f.K = a.I;

@@ -41,6 +41,7 @@ struct FewArgs {
   int slots;                       // 1..kFewSlots
   int top;                         // slots per row of x
   int rows;                        // rows of x
+  int per_token;                   // rows of x a token has (a layer's second launch: K)
   int experts;
   int N;                           // output channels (a layer's first launch: I of the 2I rows)
   int K;                           // input channels
