@@ -28,7 +28,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 constexpr uint32_t kOob = 0x80000000u;      // past every descriptor's range (< 2^31 bytes)
-constexpr int kNonTemporal = 2;             // cache policy bit of the buffer loads
 
 __device__ __forceinline__ rsrc_t make_rsrc(const void* p, int64_t bytes) {
   // stride 0, 32-bit data format: offsets are bytes, checked against `bytes`
@@ -41,15 +40,17 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 template <int KIND>
+constexpr bool kIsBf16 = KIND == kWBf16 || KIND == kWBf16Stream;
+template <int KIND>
 constexpr bool kIsInt4 = KIND == kWInt4G32 || KIND == kWInt4G64 || KIND == kWInt4G128;
 
 // Channels of a 16-byte vector's 64-byte share of a row: 32 bf16 or 128 4-bit.
 template <int KIND>
-constexpr int kVecK = KIND == kWBf16 ? 32 : 128;
+constexpr int kVecK = kIsBf16<KIND> ? 32 : 128;
 
 // Bytes of one weight row and of its scales, and scale bytes per 128 channels.
 template <int KIND>
-__device__ __forceinline__ int row_bytes(int K) { return KIND == kWBf16 ? 2 * K : K / 2; }
+__device__ __forceinline__ int row_bytes(int K) { return kIsBf16<KIND> ? 2 * K : K / 2; }
 template <int KIND>
 constexpr int kScaleBytes =
     KIND == kWFp4 ? 4 : KIND == kWInt4G32 ? 8 : KIND == kWInt4G64 ? 4 : 2;
@@ -134,12 +135,12 @@ __device__ __forceinline__ u32x4 order_x(u32x4 x) {
 
 // ---------------------------------------------------------------------------
 // A stage of weights: NV 16-byte vectors a lane of each tile of 16 rows.
-// Vector q of lane group g is bytes 64q + 16g.. of the stage, but a load that
-// takes 64 bytes of 16 rows moves memory at 4.1-5 TB/s where one that takes 128
-// bytes of 8 rows, non-temporal, moves it at 6.1 (a plain 125 MB read; the
-// non-temporal hint with 64 bytes is the slowest of all).  So a pair of
-// vectors is loaded as rows 0-7 and rows 8-15, the lanes n >= 8 of a tile
-// taking the second vector's share, and the halves change places afterwards.
+// Vector q of lane group g is bytes 64q + 16g.. of the stage.  Loads that take
+// whole 128-byte lines may carry the non-temporal hint, which moves memory
+// faster (a read of 125 MB: 6.1 against 5.0 TB/s); with 64 bytes of 16 rows the
+// hint makes it slowest of all (4.1).  So a pair of vectors is loaded as rows
+// 0-7 and rows 8-15, the lanes n >= 8 of a tile taking the second vector's
+// share, and the halves change places afterwards.
 // One scale load covers the stage, lane group g taking vector g's: loaded
 // vector by vector, the few bytes of each row cost more requests than the
 // weights (fp4 at 7168 channels: 38 against 26 us).
@@ -195,13 +196,13 @@ __device__ __forceinline__ void load_stage(Stage<KIND, NT, NV>& stage, rsrc_t wr
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int i = 0; i < NV; i += 2) {
-      const bool ok = (i + up) * kVecK<KIND> + (KIND == kWBf16 ? g * 8 : 0) < left;
+      const bool ok = (i + up) * kVecK<KIND> + (kIsBf16<KIND> ? g * 8 : 0) < left;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         stage.v[nt][i + h] = __builtin_amdgcn_raw_buffer_load_b128(
-            wr, (ok ? rows.w[nt][h] : kOob) + i * 64, so, kNonTemporal);
+            wr, (ok ? rows.w[nt][h] : kOob) + i * 64, so, KIND == kWBf16Stream ? 2 : 0);
     }
-    if constexpr (KIND != kWBf16) {
+    if constexpr (!kIsBf16<KIND>) {
       const uint32_t off = (g & (NV - 1)) * 128 < left ? rows.s[nt] : kOob;
       if constexpr (KIND == kWInt4G128) {
         stage.s[nt][0] = uint32_t(uint16_t(__builtin_amdgcn_raw_buffer_load_b16(sr, off, ss, 0)));
@@ -241,7 +242,7 @@ __device__ __forceinline__ void open_stage(Stage<KIND, NT, NV>& st, Scales<KIND,
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int q = 0; q < NV; q += 2) exchange_halves(st.v[nt][q], st.v[nt][q + 1]);
-    if constexpr (KIND != kWBf16) spread_groups<NV>(st.s[nt][0], sc.s0[nt]);
+    if constexpr (!kIsBf16<KIND>) spread_groups<NV>(st.s[nt][0], sc.s0[nt]);
     if constexpr (KIND == kWInt4G32) spread_groups<NV>(st.s[nt][1], sc.s1[nt]);
   }
 }
@@ -254,7 +255,7 @@ template <int KIND, int NT, int NV, int MT, int XP, typename X, typename Use>
 __device__ __forceinline__ void vector_products(const Stage<KIND, NT, NV>& st,
                                                 const Scales<KIND, NT, NV>& scales, int q, X x,
                                                 Use use, f32x4 (&acc)[MT][NT]) {
-  if constexpr (KIND == kWBf16) {
+  if constexpr (kIsBf16<KIND>) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (!use(mt)) continue;
@@ -339,7 +340,7 @@ constexpr int kFewRows = 4;
 
 // Blocks of 128 channels of x a stage needs.
 template <int KIND, int NV>
-constexpr int kXBlocks = KIND == kWBf16 ? NV / 4 : NV;
+constexpr int kXBlocks = kIsBf16<KIND> ? NV / 4 : NV;
 // 16-byte pieces from row to row: the four rows and four lane groups that a
 // fragment reads at once then lie in different banks.
 template <int KIND>
@@ -352,7 +353,7 @@ __device__ __forceinline__ void own_tile(rsrc_t xr, uint32_t xoff, int plane, u3
                                          rsrc_t wr, rsrc_t sr, const Rows<NT>& rows, int K, int st0,
                                          int st1, int step, f32x4 (&acc)[1][NT]) {
   constexpr int XB = kXBlocks<KIND, NV>;
-  static_assert(KIND != kWBf16 || NV % 4 == 0, "a stage holds whole blocks of x");
+  static_assert(!kIsBf16<KIND> || NV % 4 == 0, "a stage holds whole blocks of x");
   const int lane = lane_id();
   Stage<KIND, NT, NV> w[D];
   u32x4 xb[D][XB][XP];
@@ -393,7 +394,7 @@ __device__ __forceinline__ void own_tile(rsrc_t xr, uint32_t xoff, int plane, u3
             w[d], sc, q,
             [&](int, int p, int j) {
               const int g = lane >> 4;
-              const int b = KIND == kWBf16 ? q / 4 : q, i = KIND == kWBf16 ? q % 4 : j;
+              const int b = kIsBf16<KIND> ? q / 4 : q, i = kIsBf16<KIND> ? q % 4 : j;
               const int piece = kSplit<KIND> ? g * 4 + i : i * 4 + g;
               return xs[((b * XP + p) * kFewRows + (lane & 3)) * kXPitch<KIND> + piece];
             },
@@ -525,7 +526,7 @@ __device__ __forceinline__ rsrc_t matrix_rsrc(const Weights& w, int e, int rows,
 }
 template <int KIND>
 __device__ __forceinline__ rsrc_t scale_rsrc(const Weights& w, int e, int rows, int K) {
-  if (KIND == kWBf16) return make_rsrc(w.q, 0);        // not read
+  if (kIsBf16<KIND>) return make_rsrc(w.q, 0);        // not read
   const int64_t bytes = int64_t(rows) * scale_bytes<KIND>(K);
   return make_rsrc(static_cast<const char*>(w.scale) + e * bytes, bytes);
 }
@@ -541,8 +542,9 @@ template <int KIND, int NT, int NV, int W, int OUT, int D>
 __global__ __launch_bounds__(W * kWave) void few_thin_kernel(FewArgs a) {
   constexpr bool GATED = OUT == kOutGated;
   constexpr int C = GATED ? NT / 2 : NT;               // tiles of output channels
+  constexpr int XP = OUT == kOutF32 ? 2 : 1;           // h has two parts
   __shared__ SharedPlan sp;
-  __shared__ u32x4 xs[W][kXPieces<KIND, NV, 1>];
+  __shared__ u32x4 xs[W][kXPieces<KIND, NV, XP>];
   __shared__ float red[W][kFewRows][NT * 16];
   const int lane = lane_id(), wave = wave_id();
   int e = 0, first = 0, active = 0;
@@ -551,26 +553,26 @@ __global__ __launch_bounds__(W * kWave) void few_thin_kernel(FewArgs a) {
   m = __builtin_amdgcn_readfirstlane(m);
   if (GATED && blockIdx.x == 0) write_plan<W * kWave>(sp, a, e, first, m, active);
   const int n0 = blockIdx.x * (C * 16);
-  if (!GATED && blockIdx.y == 0) zero_unnamed<C * 16, W * kWave>(sp, a, n0);
+  if (OUT == kOutBf16 && blockIdx.y == 0) zero_unnamed<C * 16, W * kWave>(sp, a, n0);
   if (m == 0) return;
 
   const int all = GATED ? 2 * a.N : a.N;
   const rsrc_t wr = matrix_rsrc<KIND>(a.w, e, all, a.K);
   const rsrc_t sr = scale_rsrc<KIND>(a.w, e, all, a.K);
-  const rsrc_t xr = make_rsrc(a.x, int64_t(a.rows) * a.K * 2);
+  const rsrc_t xr = make_rsrc(a.x, int64_t(a.rows) * a.K * (2 * XP));
   Rows<NT> rows;
   set_rows<KIND, NT, NV>(
       rows, a.K, [&](int nt) { return n0 + (nt % C) * 16 + (nt >= C ? a.N : 0); }, n0, a.N, C);
   const int stages = (a.K + NV * kVecK<KIND> - 1) / (NV * kVecK<KIND>);
   for (int c0 = 0; c0 < m; c0 += kFewRows) {
     const int i = c0 + (lane >> 4);
-    const uint32_t xoff = i < m ? uint32_t(sp.list[i] / a.top) * uint32_t(a.K * 2) +
+    const uint32_t xoff = i < m ? uint32_t(sp.list[i] / a.top) * uint32_t(a.K * 2 * XP) +
                                       uint32_t(lane & 15) * 16u
                                 : kOob;
     f32x4 acc[1][NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[0][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    own_tile<KIND, NT, NV, 1, D>(xr, xoff, 0, xs[wave], wr, sr, rows, a.K, wave, stages, W, acc);
+    own_tile<KIND, NT, NV, XP, D>(xr, xoff, a.K * 2, xs[wave], wr, sr, rows, a.K, wave, stages, W, acc);
     if (c0 > 0) __syncthreads();                       // the last rows' sums have been read
     if (lane < 16) {                                   // lane l: channel l of rows 0..3
 #pragma unroll
@@ -592,8 +594,10 @@ __global__ __launch_bounds__(W * kWave) void few_thin_kernel(FewArgs a) {
       const int64_t slot = sp.list[c0 + r];
       if constexpr (GATED)
         store_h(static_cast<__bf16*>(a.y) + slot * (2 * a.N) + n0 + c, a.N, v, u);
-      else
+      else if constexpr (OUT == kOutBf16)
         static_cast<__bf16*>(a.y)[slot * a.N + n0 + c] = __bf16(v);
+      else
+        static_cast<float*>(a.y)[slot * a.N + n0 + c] = v;
     }
   }
 }
@@ -707,7 +711,7 @@ __global__ __launch_bounds__(kBlock, 2) void few_wide_kernel(FewArgs a) {
             vector_products<KIND, NT, NV, MT, XP>(
                 w[d], sc, q,
                 [&](int mt, int p, int j) {
-                  const int f = KIND == kWBf16 ? q % 4 : j, g = lane >> 4;
+                  const int f = kIsBf16<KIND> ? q % 4 : j, g = lane >> 4;
                   const int c = kSplit<KIND> ? g * 4 + f : f * 4 + g;
                   return xs[buf][mt][p][f][g * 16 + ((lane + c) & 15)];
                 },
@@ -753,7 +757,7 @@ __global__ __launch_bounds__(kBlock, 2) void few_wide_kernel(FewArgs a) {
 constexpr int kDownWaves = 8;
 constexpr int kDownBlock = kDownWaves * kWave;
 constexpr int kDownMaxSplit = 8;
-constexpr int kDownSlots = 64;                         // most slots: kFewRows tokens of 16
+constexpr int kDownSlots = 64;                         // most slots
 
 template <int KIND, int NT, int NV, int D>
 __global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a) {
@@ -818,14 +822,15 @@ __global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a) {
     }
   }
   __syncthreads();
-  if (tid < a.T * C && n0 + tid % C < a.H) {           // at most kFewRows * C threads
-    const int t = tid / C, ch = n0 + tid % C;
+  for (int i = tid; i < a.T * C; i += kDownBlock) {
+    const int t = i / C, ch = n0 + i % C;
+    if (ch >= a.H) continue;
     float sum = 0.f;
     for (int k = 0; k < a.K; ++k) {
       const int s = t * a.K + k;
       if (!local[s]) continue;
       float y = 0.f;
-      for (int p = 0; p < split; ++p) y += prod[(p * slots + s) * C + tid % C];
+      for (int p = 0; p < split; ++p) y += prod[(p * slots + s) * C + i % C];
       sum += weight[s] * y;
     }
     const int64_t o = int64_t(t) * a.H + ch;
@@ -949,7 +954,7 @@ constexpr int kCus = 256;
 template <int KIND, int NT, int MT, int OUT>
 hipError_t launch_wide(const FewArgs& a, hipStream_t s) {
   constexpr int C = (OUT == kOutGated ? NT / 2 : NT) * 16 * kWavesPerBlock;
-  constexpr int NV = KIND == kWBf16 ? 4 : 2;           // 256 bytes of a bf16 row, 128 of a 4-bit one
+  constexpr int NV = kIsBf16<KIND> ? 4 : 2;           // 256 bytes of a bf16 row, 128 of a 4-bit one
   constexpr int XP = OUT == kOutF32 ? 2 : 1;
   const dim3 grid(unsigned((a.N + C - 1) / C), most_experts(a));
   few_wide_kernel<KIND, NT, NV, MT, XP, OUT, 2><<<grid, kBlock, 0, s>>>(a);
@@ -970,10 +975,10 @@ template <int KIND, int OUT>
 hipError_t wide_variant(const FewArgs& a, hipStream_t s) {
   constexpr int half = OUT == kOutGated ? 2 : 1;       // a gate and an up tile an output tile
   const int average = (a.slots + a.experts - 1) / a.experts;
-  const int mt = a.rows <= 16 * (OUT == kOutF32 ? a.per_token : 1) || average <= 12 ? 1
+  const int mt = a.rows <= 16 * a.per_token || average <= 12 ? 1
                  : average < 28 ? 2 : 3;
   if (mt == 3) return launch_wide<KIND, 2, 3, OUT>(a, s);
-  if constexpr (KIND == kWBf16) {
+  if constexpr (kIsBf16<KIND>) {
     if (groups_of(a, 4 / half * 64) >= kCus * 3 / 4)
       return mt == 1 ? launch_wide<KIND, 4, 1, OUT>(a, s) : launch_wide<KIND, 4, 2, OUT>(a, s);
   }
@@ -987,7 +992,7 @@ hipError_t wide_variant(const FewArgs& a, hipStream_t s) {
 template <int KIND, int OUT, int W>
 hipError_t launch_thin(const FewArgs& a, hipStream_t s) {
   constexpr int NT = OUT == kOutGated ? 2 : 1;
-  constexpr int NV = KIND == kWBf16 ? 4 : 2;
+  constexpr int NV = kIsBf16<KIND> ? 4 : 2;
   const dim3 grid(unsigned((a.N + 15) / 16), most_experts(a));
   few_thin_kernel<KIND, NT, NV, W, OUT, 2><<<grid, W * kWave, 0, s>>>(a);
   return hipGetLastError();
@@ -1002,13 +1007,30 @@ hipError_t thin_variant(const FewArgs& a, hipStream_t s) {
   return launch_thin<KIND, OUT, 4>(a, s);
 }
 
+// Thin where an expert's rows come to one pass of four anyway, or where the
+// wide form would leave most of the chip idle; not where the channels are too
+// few for its four waves.
+template <int KIND, int OUT>
+bool takes_thin(const FewArgs& a) {
+  if (a.rows <= kFewRows * a.per_token) return true;
+  if (a.K < (kIsBf16<KIND> ? 512 : 1024)) return false;
+  const int average = (a.slots + a.experts - 1) / a.experts;
+  const int64_t groups = groups_of(a, OUT == kOutGated ? 64 : 128);
+  return average <= 2 || (groups < 192 && average <= 6) || (groups < 48 && average <= 16);
+}
+
+template <int KIND, int OUT>
+hipError_t rows_variant(const FewArgs& a, hipStream_t s) {
+  return takes_thin<KIND, OUT>(a) ? thin_variant<KIND, OUT>(a, s) : wide_variant<KIND, OUT>(a, s);
+}
+
 // The down products of up to four tokens: 32 channels a workgroup for 4-bit
 // weights if that leaves enough workgroups, else 16 (one token, 8 fp4 experts
 // of 7168 x 2048: 19.9 against 22.5 us; bf16, 512 x 256: 7.3 against 5.8).
 template <int KIND, int NT>
 hipError_t launch_down(const DownArgs& a, hipStream_t s) {
   constexpr int C = NT * 16;
-  constexpr int NV = KIND == kWBf16 ? 4 : 2;
+  constexpr int NV = kIsBf16<KIND> ? 4 : 2;
   few_down_kernel<KIND, NT, NV, 2>
       <<<dim3(unsigned((a.H + C - 1) / C)), kDownBlock,
          size_t(kDownMaxSplit) * size_t(a.T * a.K) * C * 4, s>>>(a);
@@ -1017,7 +1039,7 @@ hipError_t launch_down(const DownArgs& a, hipStream_t s) {
 
 template <int KIND>
 hipError_t down_variant(const DownArgs& a, hipStream_t s) {
-  if constexpr (KIND != kWBf16)
+  if constexpr (!kIsBf16<KIND>)
     if (a.H >= 32 * kCus * 3 / 4) return launch_down<KIND, 2>(a, s);
   return launch_down<KIND, 1>(a, s);
 }
@@ -1027,6 +1049,7 @@ template <typename Fn>
 hipError_t with_kind(WeightKind kind, Fn fn) {
   switch (kind) {
     case kWBf16: return fn(std::integral_constant<int, kWBf16>());
+    case kWBf16Stream: return fn(std::integral_constant<int, kWBf16Stream>());
     case kWFp4: return fn(std::integral_constant<int, kWFp4>());
     case kWInt4G32: return fn(std::integral_constant<int, kWInt4G32>());
     case kWInt4G64: return fn(std::integral_constant<int, kWInt4G64>());
@@ -1036,20 +1059,37 @@ hipError_t with_kind(WeightKind kind, Fn fn) {
 
 }  // namespace
 
-bool few_is_wide(int rows) { return rows > kFewRows; }
+// Whether bf16 matrices are read with the non-temporal hint: rows of whole
+// 128-byte lines, and more of them than the last-level cache (256 MB) could
+// hold beside anything else.  With both, 48 rows of 8 matrices of 7168 x 2048
+// took 48.8 against 52.3 us; rows that start inside a line fetch it twice under
+// the hint (a layer of 7160 channels: 161 against 148 us), and 40 MB of
+// matrices stay in the cache without it (14.7 against 21.7).  The 4-bit
+// formats gain 4 % at most and are read plainly.
+WeightKind stream_kind(const Weights& w, int experts, int rows, int K) {
+  if (w.kind != kWBf16) return w.kind;
+  const int64_t bytes = int64_t(experts) * rows * K * 2;
+  return K % 64 == 0 && reinterpret_cast<uintptr_t>(w.q) % 128 == 0 && bytes >= (128 << 20)
+             ? kWBf16Stream
+             : kWBf16;
+}
+
+bool few_down_joined(int slots, int hidden, int inner) {
+  // few output channels make few workgroups, each of which reads every expert
+  return slots <= kDownSlots && (hidden >= 2048 || slots * int64_t(inner) <= 8192);
+}
 
 hipError_t launch_few_rows(const FewArgs& a, bool gated, hipStream_t s) {
-  return with_kind(a.w.kind, [&](auto kind) {
+  return with_kind(stream_kind(a.w, a.experts, gated ? 2 * a.N : a.N, a.K), [&](auto kind) {
     constexpr int KIND = decltype(kind)::value;
-    if (few_is_wide(a.rows))
-      return gated ? wide_variant<KIND, kOutGated>(a, s) : wide_variant<KIND, kOutBf16>(a, s);
-    return gated ? thin_variant<KIND, kOutGated>(a, s) : thin_variant<KIND, kOutBf16>(a, s);
+    return gated ? rows_variant<KIND, kOutGated>(a, s) : rows_variant<KIND, kOutBf16>(a, s);
   });
 }
 
 hipError_t launch_few_down(const DownArgs& a, hipStream_t s) {
-  if (!few_is_wide(a.T))
-    return with_kind(a.w.kind, [&](auto kind) {
+  const WeightKind kind_now = stream_kind(a.w, a.experts, a.H, a.I);
+  if (few_down_joined(a.T * a.K, a.H, a.I))
+    return with_kind(kind_now, [&](auto kind) {
       return down_variant<decltype(kind)::value>(a, s);
     });
   FewArgs f{};
@@ -1065,8 +1105,8 @@ hipError_t launch_few_down(const DownArgs& a, hipStream_t s) {
   f.K = a.I;
   f.w = a.w;
   f.y = a.y;
-  const hipError_t e = with_kind(a.w.kind, [&](auto kind) {
-    return wide_variant<decltype(kind)::value, kOutF32>(f, s);
+  const hipError_t e = with_kind(kind_now, [&](auto kind) {
+    return rows_variant<decltype(kind)::value, kOutF32>(f, s);
   });
   if (e != hipSuccess) return e;
   const dim3 grid(unsigned((a.H / 4 + kBlock - 1) / kBlock), unsigned(a.T));

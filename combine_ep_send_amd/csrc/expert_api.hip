@@ -107,6 +107,7 @@ int ep_expert_matvec(const void* x, const int32_t* row_expert, int64_t num_rows,
   a.slots = int(num_rows);
   a.top = 1;
   a.rows = int(num_rows);
+  a.per_token = 1;
   a.experts = num_experts;
   a.N = out_channels;
   a.K = channels;
@@ -123,7 +124,7 @@ size_t ep_moe_tokens_workspace_bytes(int64_t num_tokens, int num_topk, int hidde
     return 0;
   const size_t slots = size_t(num_tokens) * size_t(num_topk);
   return kPlanBytes + h_bytes(slots, inner) +
-         (few_is_wide(int(num_tokens)) ? slots * size_t(hidden) * 4 : 0);
+         (few_down_joined(int(slots), hidden, inner) ? 0 : slots * size_t(hidden) * 4);
 }
 
 int ep_moe_tokens(const void* x, const int64_t* topk_idx, const float* topk_weights,
@@ -162,6 +163,7 @@ int ep_moe_tokens(const void* x, const int64_t* topk_idx, const float* topk_weig
   a.slots = int(num_tokens) * num_topk;
   a.top = num_topk;
   a.rows = int(num_tokens);
+  a.per_token = 1;
   a.experts = num_local_experts;
   a.N = inner;
   a.K = hidden;

@@ -12,7 +12,10 @@ constexpr int kFewSlots = 1024;    // slots (token, k) or rows of one call
 constexpr int kFewExperts = 1024;
 
 // One kind of weights of the few-row products.
-enum WeightKind : int { kWBf16 = 0, kWFp4 = 1, kWInt4G32 = 2, kWInt4G64 = 3, kWInt4G128 = 4 };
+// kWBf16Stream: bf16 read with the non-temporal hint, chosen at the launch.
+enum WeightKind : int {
+  kWBf16 = 0, kWFp4 = 1, kWInt4G32 = 2, kWInt4G64 = 3, kWInt4G128 = 4, kWBf16Stream = 5
+};
 
 struct Weights {
   WeightKind kind;
@@ -64,11 +67,11 @@ struct DownArgs {
   const void* bias0;
   const void* bias1;
   void* out;
-  float* y;                        // [slots, H], used by the wide form
+  float* y;                        // [slots, H], where the sum is a launch of its own
 };
-// Whether calls of so many rows (a layer: tokens) take the wide form, whose
-// workspace holds y.
-bool few_is_wide(int rows);
+// Whether a layer of so many slots sums its down products in the launch that
+// makes them; otherwise they go through y in its workspace.
+bool few_down_joined(int slots, int hidden, int inner);
 hipError_t launch_few_down(const DownArgs& a, hipStream_t s);
 
 struct QuantArgs {

@@ -76,7 +76,7 @@ def _on(t, name: str, dtype, shape, index: int) -> torch.Tensor:
 
 
 def _elsewhere(index: int, stream) -> bool:
-    return stream is not None or index != torch.cuda.current_device()
+    return stream is not None or index != torch._C._cuda_getDevice()
 
 
 def _there(fn, index: int, stream, *args, **kw):
@@ -217,7 +217,7 @@ def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.T
         ptrs = [_on(b, f"bias[{i}]", _BF16, (T, H), index).data_ptr() for i, b in enumerate(pair)]
         b0, b1 = (ptrs + [None, None])[:2]
     if out is None:
-        out = x.new_empty((T, H))
+        out = torch.empty_like(x)
     else:
         _on(out, "out", _BF16, (T, H), index)
     if workspace is None:
