@@ -969,8 +969,9 @@ hipError_t launch_wide(const FewArgs& a, hipStream_t s) {
 // are likely.  Weight rows: two tiles a wave; four for bf16 if that still
 // gives most compute units a workgroup (48 rows, 8 matrices of 7168 x 2048: 41
 // us against 48; 128 workgroups instead of 256 took 30 against 19; 4-bit ones
-// need too many registers: 740 against 435), and one for a matrix too small
-// for half the units (9 rows, 4 fp4 matrices of 1000 x 640: 6.2 against 7.6).
+// need too many registers: 740 against 435), and one where two would leave half
+// the units idle (9 rows, 4 fp4 matrices of 1000 x 640: 6.2 against 7.6; 42 rows,
+// 2 int4 matrices of 4648 x 3328: 20 against 47).
 template <int KIND, int OUT>
 hipError_t wide_variant(const FewArgs& a, hipStream_t s) {
   constexpr int half = OUT == kOutGated ? 2 : 1;       // a gate and an up tile an output tile
@@ -982,7 +983,7 @@ hipError_t wide_variant(const FewArgs& a, hipStream_t s) {
     if (groups_of(a, 4 / half * 64) >= kCus * 3 / 4)
       return mt == 1 ? launch_wide<KIND, 4, 1, OUT>(a, s) : launch_wide<KIND, 4, 2, OUT>(a, s);
   }
-  if constexpr (OUT == kOutBf16) {
+  if constexpr (OUT != kOutGated) {
     if (groups_of(a, 128) < kCus / 2)
       return mt == 1 ? launch_wide<KIND, 1, 1, OUT>(a, s) : launch_wide<KIND, 1, 2, OUT>(a, s);
   }

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kBlock) void swiglu_fp8_backward_kernel(SwigluArgs 
 // token reads, keeps the products' sums and stores the scaled piece; the
 // workgroup then adds the sums up, lanes first, waves in order.
 // ---------------------------------------------------------------------------
-constexpr int kGradMaxBlock = 1024;
+constexpr int kGradMaxBlock = 512;
 
 template <int KMAX, bool WEIGHTED, bool DOT>
 __global__ __launch_bounds__(kGradMaxBlock) void combine_backward_kernel(CombineBackwardArgs a,
