@@ -533,7 +533,7 @@ __device__ __forceinline__ rsrc_t scale_rsrc(const Weights& w, int e, int rows, 
 
 // ---------------------------------------------------------------------------
 // Up to four rows an expert at a time: grid (tiles of weight rows, experts in
-// use at most).  The four waves of a workgroup take every fourth stage of the
+// use at most).  The W waves of a workgroup take every W-th stage of the
 // channels each, which spreads a small matrix over more of the chip, and add
 // up through LDS in a fixed order.  kOutGated: a tile is half gate and half up
 // rows.
@@ -572,7 +572,8 @@ __global__ __launch_bounds__(W * kWave) void few_thin_kernel(FewArgs a) {
     f32x4 acc[1][NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[0][nt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    own_tile<KIND, NT, NV, XP, D>(xr, xoff, a.K * 2, xs[wave], wr, sr, rows, a.K, wave, stages, W, acc);
+    own_tile<KIND, NT, NV, XP, D>(xr, xoff, a.K * 2, xs[wave], wr, sr, rows, a.K, wave, stages, W,
+                                  acc);
     if (c0 > 0) __syncthreads();                       // the last rows' sums have been read
     if (lane < 16) {                                   // lane l: channel l of rows 0..3
 #pragma unroll
@@ -611,7 +612,7 @@ __device__ __forceinline__ void lds_barrier() {
 
 // ---------------------------------------------------------------------------
 // The same for more rows: the four waves of a workgroup own different weight
-// rows and share the rows x, which each fetches a quarter of and passes on
+// rows and share the rows x, which each fetches its part of and passes on
 // through LDS, stage by stage.  A row x then comes out of the L2 once for
 // 64*NT weight rows.
 // ---------------------------------------------------------------------------
@@ -749,8 +750,8 @@ __global__ __launch_bounds__(kBlock, 2) void few_wide_kernel(FewArgs a) {
 
 // ---------------------------------------------------------------------------
 // Second launch of a layer of a few slots: the down products and the weighted
-// sum.  A workgroup owns 16 output channels of every token, so the sum over a
-// token's experts needs no atomics: its eight waves share out (expert, part of
+// sum.  A workgroup owns 16*NT output channels of every token, so the sum over
+// a token's experts needs no atomics: its eight waves share out (expert, part of
 // the channels) and leave each slot's products in LDS, then one thread per
 // (token, channel) adds them up in the order of the slots.
 // ---------------------------------------------------------------------------
@@ -840,8 +841,8 @@ __global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a) {
   }
 }
 
-// The weighted sum of the slots' products y [slots, H], after the wide form of
-// the down products: one thread per token and four channels.
+// The weighted sum of the slots' products y [slots, H], where the down products
+// are a launch of their own: one thread per token and four channels.
 __global__ __launch_bounds__(kBlock) void few_sum_kernel(DownArgs a) {
   const int t = blockIdx.y;
   const int c = (blockIdx.x * kBlock + threadIdx.x) * 4;
@@ -886,8 +887,9 @@ __device__ __forceinline__ uint32_t e2m1_code(float v) {
 }
 
 template <bool FP4>
-__global__ __launch_bounds__(kBlock) void quantize_w4_kernel(QuantArgs a, int64_t pieces) {
-  const int64_t p = int64_t(blockIdx.x) * kBlock + threadIdx.x;
+__global__ __launch_bounds__(kBlock) void quantize_w4_kernel(QuantArgs a, int64_t block0,
+                                                             int64_t pieces) {
+  const int64_t p = (block0 + blockIdx.x) * kBlock + threadIdx.x;
   const bool in = p < pieces;                // a group's lanes are all in or all out
   u32x4 v = {0u, 0u, 0u, 0u};
   if (in) v = static_cast<const u32x4*>(a.w)[p];
@@ -1010,7 +1012,12 @@ hipError_t thin_variant(const FewArgs& a, hipStream_t s) {
 
 // Thin where an expert's rows come to one pass of four anyway, or where the
 // wide form would leave most of the chip idle; not where the channels are too
-// few for its four waves.
+// few for its four waves.  Thin against wide, whole calls in a graph: a layer of
+// 7 tokens, 27 bf16 experts of 3928 x 1408, 92 against 118 us; of 10 tokens, 26
+// of 5392 x 144, 26 against 51; 8 rows, 9 int4 matrices of 96 x 5760, 7.6
+// against 20.  The other way round: 76 rows, 9 bf16 matrices of 2040 x 3368, 54
+// against 42; a layer of 32 tokens, 29 int4 experts of 640 x 896, 45 against 27;
+// 8 rows, 10 bf16 matrices of 5632 x 232, 9.6 against 7.5.
 template <int KIND, int OUT>
 bool takes_thin(const FewArgs& a) {
   if (a.rows <= kFewRows * a.per_token) return true;
@@ -1025,8 +1032,8 @@ hipError_t rows_variant(const FewArgs& a, hipStream_t s) {
   return takes_thin<KIND, OUT>(a) ? thin_variant<KIND, OUT>(a, s) : wide_variant<KIND, OUT>(a, s);
 }
 
-// The down products of up to four tokens: 32 channels a workgroup for 4-bit
-// weights if that leaves enough workgroups, else 16 (one token, 8 fp4 experts
+// The joined down products: 32 channels a workgroup for 4-bit weights if that
+// leaves enough workgroups, else 16 (one token, 8 fp4 experts
 // of 7168 x 2048: 19.9 against 22.5 us; bf16, 512 x 256: 7.3 against 5.8).
 template <int KIND, int NT>
 hipError_t launch_down(const DownArgs& a, hipStream_t s) {
@@ -1075,9 +1082,18 @@ WeightKind stream_kind(const Weights& w, int experts, int rows, int K) {
              : kWBf16;
 }
 
+// Products and sum in one launch for a few slots (it saves a launch and y),
+// unless few output channels would make few workgroups, each of which reads its
+// rows of every expert: 5 tokens, 30 slots of 384 x 1664 int4 experts take 39 us
+// joined and 19 apart.  With more than 32 slots the wide form shares weights that
+// this one reads per pass, unless the products are too small for that to show: 64
+// slots of 13 fp4 experts of 3456 x 1664, 64 us joined and 52 apart; of 64 experts
+// of 7168 x 2048, 300 and 268; but 32 slots of 32 int4 experts of 4096 x 1024, 51
+// and 72; 18 slots of 15 bf16 experts of 4888 x 136, 17 and 20.  The price: with
+// most experts elsewhere, 42 slots of 5888 x 768, 25 joined and 27 apart.
 bool few_down_joined(int slots, int hidden, int inner) {
-  // few output channels make few workgroups, each of which reads every expert
-  return slots <= kDownSlots && (hidden >= 2048 || slots * int64_t(inner) <= 8192);
+  return (slots <= kDownSlots / 2 && hidden >= 2048) ||
+         (slots <= kDownSlots && slots * int64_t(inner) <= 8192);
 }
 
 hipError_t launch_few_rows(const FewArgs& a, bool gated, hipStream_t s) {
@@ -1117,12 +1133,15 @@ hipError_t launch_few_down(const DownArgs& a, hipStream_t s) {
 
 hipError_t launch_quantize_w4(const QuantArgs& a, hipStream_t s) {
   const int64_t pieces = a.rows * (a.channels / 8);
-  // at most 2^31 - 1 workgroups a launch; the caller's size limit keeps below
-  const dim3 grid(unsigned((pieces + kBlock - 1) / kBlock));
-  if (a.fp4)
-    quantize_w4_kernel<true><<<grid, kBlock, 0, s>>>(a, pieces);
-  else
-    quantize_w4_kernel<false><<<grid, kBlock, 0, s>>>(a, pieces);
+  const int64_t blocks = (pieces + kBlock - 1) / kBlock;
+  constexpr int64_t kMost = int64_t(UINT32_MAX) / kBlock;      // work-items a launch, 2^32 - 1
+  for (int64_t b0 = 0; b0 < blocks; b0 += kMost) {
+    const dim3 grid(unsigned(blocks - b0 < kMost ? blocks - b0 : kMost));
+    if (a.fp4)
+      quantize_w4_kernel<true><<<grid, kBlock, 0, s>>>(a, b0, pieces);
+    else
+      quantize_w4_kernel<false><<<grid, kBlock, 0, s>>>(a, b0, pieces);
+  }
   return hipGetLastError();
 }
 

@@ -185,11 +185,11 @@ def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.T
                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                   stream=None) -> torch.Tensor:
     """out [T, H] bf16 of a whole expert layer for up to 128 tokens (T*K up to
-    1024), in two launches (three for more than four tokens): out[t] = sum over
-    the slots whose expert e = topk_idx[t, k] - first_expert is one of the E
-    here of topk_weights[t, k] * W2[e] (silu(gate) * up), the gate and up rows
-    being W13[e] x[t].  ``w13`` [E, 2I, H] (the gate rows, then the up rows) and
-    ``w2`` [E, H, I] are bf16 or W4Weights; ``bias`` is a [T, H] bf16 tensor or
+    1024), in two or three launches: out[t] = sum over the slots whose expert e =
+    topk_idx[t, k] - first_expert is one of the E here of topk_weights[t, k] *
+    W2[e] (silu(gate) * up), the gate and up rows being W13[e] x[t].  ``w13``
+    [E, 2I, H] (the gate rows, then the up rows) and ``w2`` [E, H, I] are bf16 or
+    W4Weights; ``bias`` is a [T, H] bf16 tensor or
     a pair, added in fp32 before the one rounding, as in ep_combine.
 
     Without ``workspace`` (uint8, ep_moe_tokens_workspace_bytes of it) each

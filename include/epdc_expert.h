@@ -79,8 +79,8 @@ int ep_quantize_w4(const void* w, int64_t num_rows, int channels, int weight_fmt
  * Products of a few rows with their experts' matrices:
  *   y[r,:] = bf16( W[row_expert[r]] x[r,:] ),
  * products and sums in fp32, rounded once.  The weights of an expert that
- * several rows name are read from memory once for up to 32 of them.  Rows
- * whose id lies outside [0, E) get +0.
+ * several rows name are read once for 4 to 48 of them, by the sizes.  Rows whose
+ * id lies outside [0, E) get +0.
  * An int4 product computes sum (c + 16 - 24) x as a difference of two sums,
  * so that its x must stay below 2^122 in magnitude; an infinite or NaN
  * channel of a row gives that row NaN.
@@ -107,8 +107,9 @@ int ep_expert_matvec(const void* x, const int32_t* row_expert, int64_t num_rows,
 size_t ep_moe_tokens_workspace_bytes(int64_t num_tokens, int num_topk, int hidden, int inner);
 
 /*
- * A whole expert layer for a few tokens, in two launches (three for more than
- * four tokens): with e = topk_idx[t,k] - first_expert, for every slot whose e lies in [0, E_local),
+ * A whole expert layer for a few tokens, in two launches, or three where the
+ * sum over a token's experts is one of its own: with e = topk_idx[t,k] -
+ * first_expert, for every slot whose e lies in [0, E_local),
  *   h[t,k,:] = silu(g) * u,  g = W13[e][0:I] x[t],  u = W13[e][I:2I] x[t]
  *   out[t,:] = bf16( sum_k w[t,k] * (W2[e] h[t,k,:]) + bias0[t,:] + bias1[t,:] )
  * silu(g) = g / (1 + exp(-g)).  Products and sums are in fp32: each slot's

@@ -263,6 +263,44 @@ def test_layer_gives_the_same_bits_again_and_keeps_to_its_buffers(tokens):
         assert torch.equal(first.view(torch.int16), again.view(torch.int16))
 
 
+@pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("T,K,E,H,I", [(4, 16, 64, 6272, 128), (8, 8, 9, 6272, 128),
+                                       (16, 4, 2, 2176, 128), (13, 5, 3, 2176, 128),
+                                       (4, 8, 9, 2176, 384), (11, 3, 9, 2176, 384)])
+def test_layer_of_up_to_64_slots_and_many_channels(fmt, group, T, K, E, H, I):
+    """The sum joined to the products at its most slots and widest tiles, and
+    one slot past it."""
+    rng = np.random.default_rng(T + K)
+    t13, v13, m13 = make_weights(rng, fmt, group, E, 2 * I, H)
+    t2, v2, m2 = make_weights(rng, fmt, group, E, H, I)
+    x = bf16(rng.standard_normal((T, H)))
+    idx, w = topk(rng, T, K, E)
+    out = ep.ep_moe_tokens(x.to(DEV), torch.from_numpy(idx).to(DEV), torch.from_numpy(w).to(DEV),
+                           dev_weights(t13, fmt, group), dev_weights(t2, fmt, group))
+    ref, tol = moe_ref(f64(x), idx, w, v13, m13, v2, m2, 0)
+    check(out, ref, tol)
+
+
+@pytest.mark.parametrize("R", [2, 5, 40])
+def test_matrices_near_the_size_limit(R):
+    """Five matrices of 2^31 - 2^18 bytes (over 10 GB): offsets inside a matrix
+    reach the 31st bit, those of the later ones pass the 32nd."""
+    N, K = 16384, 65528
+    g = torch.Generator(device=DEV).manual_seed(1)
+    w = torch.zeros(5, N, K, dtype=torch.bfloat16, device=DEV)
+    rows = [0, 1, 8191, 8192, N - 17, N - 1]
+    w[:, rows] = torch.randn(5, len(rows), K, device=DEV, generator=g).to(torch.bfloat16)
+    x = torch.randn(R, K, device=DEV, generator=g).to(torch.bfloat16)
+    ids = torch.tensor([4, 1, 4, 0, 3] * 8, dtype=torch.int32, device=DEV)[:R]
+    y = ep.ep_expert_matvec(x, w, ids)
+    picked = f64(w[:, rows].cpu())
+    ref, tol = matvec_ref(f64(x.cpu()), ids.cpu().numpy(), picked, np.abs(picked))
+    check(y[:, rows], ref, tol)
+    rest = torch.ones(N, dtype=torch.bool, device=DEV)
+    rest[rows] = False
+    assert (y[:, rest] == 0).all()
+
+
 def test_empty_calls():
     w13 = torch.zeros(2, 16, 8, dtype=torch.bfloat16, device=DEV)
     w2 = torch.zeros(2, 8, 8, dtype=torch.bfloat16, device=DEV)
