@@ -381,6 +381,28 @@ def test_quantizer(fmt, group, rows, K):
     assert (np.abs(back - t.double().numpy())[ok] <= step[ok]).all()
 
 
+@pytest.mark.parametrize("fmt", ["int4", "fp4"])
+def test_quantizer_of_more_than_one_launch(fmt):
+    """2^32 pieces of eight channels and a few more (69 GB of bf16): the rows at
+    the ends and around the second launch's first piece as by themselves."""
+    N, K = (1 << 20) + 3, 1 << 15
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GB of device memory")
+    w = torch.zeros(N, K, dtype=torch.bfloat16, device=DEV)
+    rows = [0, 1, N // 2, N - 6, N - 5, N - 4, N - 3, N - 2, N - 1]
+    g = torch.Generator(device=DEV).manual_seed(2)
+    w[rows] = torch.randn(len(rows), K, device=DEV, generator=g).to(torch.bfloat16)
+    got = ep.ep_quantize_w4(w, fmt)
+    alone = ep.ep_quantize_w4(w[rows], fmt)
+    assert torch.equal(got.q[rows], alone.q) and torch.equal(got.scale[rows], alone.scale)
+    nothing = 0x88 if fmt == "int4" else 0
+    for r in (2, N // 4, N - 7):
+        assert (got.q[r] == nothing).all()
+        assert (got.scale[r] == 0).all()
+    del w, got, alone
+    torch.cuda.empty_cache()
+
+
 def test_quantized_matrices_in_a_layer():
     """bf16 experts quantized by the package give the layer of their values."""
     rng = np.random.default_rng(21)

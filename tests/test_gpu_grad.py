@@ -245,6 +245,21 @@ def test_combine_backward_against_differences():
             assert abs(loss(y, v) - loss(y, w) - dw[t, k]) < 1e-12
 
 
+def test_combine_backward_of_more_than_one_launch():
+    """2^26 + 5 tokens of one wave each pass the work-items of one launch."""
+    T, H = (1 << 26) + 5, 8
+    g = torch.Generator(device=DEV).manual_seed(3)
+    dout = torch.randint(-4, 5, (T, H), device=DEV, generator=g, dtype=torch.int8
+                         ).to(torch.bfloat16)
+    y = torch.randint(-4, 5, (T, H), device=DEV, generator=g, dtype=torch.int8).to(torch.bfloat16)
+    row = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    w = torch.randint(1, 4, (T, 1), device=DEV, generator=g).float()
+    dy, dw = ep.ep_combine_backward(dout, y, row, w)
+    # small integers: every product and sum is exact
+    assert torch.equal(dy, (dout.float() * w).to(torch.bfloat16).flip(0))
+    assert torch.equal(dw[:, 0], (dout.float() * y.flip(0).float()).sum(1))
+
+
 def test_combine_backward_skips_rows_outside_the_buffer():
     rng = np.random.default_rng(5)
     T, K, H, R = 4, 3, 64, 5
