@@ -3,9 +3,9 @@
  *
  * Second header of libepdc.so: what runs between the dispatch and the combine
  * of epdc.h.  The experts' products for a few rows (bf16 or 4-bit weights), a
- * whole expert layer for a few tokens in two launches, the gated activation
- * with an 8-bit checkpoint for its backward pass, and the gradient of the
- * combine.
+ * whole expert layer for a few tokens in two or three launches, the gated
+ * activation with an 8-bit checkpoint for its backward pass, and the gradient
+ * of the combine.
  *
  * The conventions are those of epdc.h: device pointers to row-major,
  * contiguous arrays; the caller owns every buffer; the library allocates
@@ -150,8 +150,8 @@ int ep_moe_tokens(const void* x, const int64_t* topk_idx, const float* topk_weig
  *              e4m3(fp32(x / scale)).
  * The rounding of the codes, zeros, NaN and infinities follow
  * ep_dispatch_permute's fp8 form, whose scale is fp32(amax / 448), at most one
- * unit in the last place from this one.  A user keeps q and scale (2I + I/16 bytes a row) instead of gate_up and h
- * (6I bytes).
+ * unit in the last place from this one.  A user keeps q and scale (2I + I/16
+ * bytes a row) instead of gate_up and h (6I bytes).
  *
  *   gate_up    [num_rows, 2I] bf16 in (16-byte aligned)
  *   row_count  [1] int32 in, device memory, or NULL: rows from row_count[0] on
