@@ -617,7 +617,7 @@ __device__ __forceinline__ void lds_barrier() {
 // rows and share the rows x, which each fetches its part of and passes on
 // through LDS, stage by stage.  A row x then comes out of the L2 once for
 // 64*NT weight rows.  bf16 is bound by the weights: 48 rows, 8 matrices of 7168
-// x 2048, 235 MB, 43 us (5.5 TB/s) a call.  32 rows for each of 32 int4 experts of
+// x 2048, 235 MB, 47 us (5.0 TB/s) a call.  32 rows for each of 32 int4 experts of
 // 7168 x 2048 take 194 us (gate and up; 137 with the loads alone, 79 with the
 // decoding and products alone) and 173 us (down; 104 and 77): the two overlap
 // only partly, as the registers allow two waves a SIMD.
@@ -976,26 +976,22 @@ hipError_t launch_wide(const FewArgs& a, hipStream_t s) {
 
 // The wide form's tiles.  Rows: an expert's rows are not known here, so the
 // average over the experts stands for them; 48 rows at a time from 28 on (32
-// rows each of 32 int4 experts of 7168 x 2048: 366 us against 435 with 32 rows
-// at a time, which read half the weights twice; 8 bf16 experts with three rows
-// each, where 25 were possible: 64 against 60), 16 where no more can come or
-// are likely.  Weight rows: two tiles a wave; four for bf16 if that still
-// gives most compute units a workgroup (48 rows, 8 matrices of 7168 x 2048: 41
-// us against 48; 128 workgroups instead of 256 took 30 against 19; 4-bit ones
-// need too many registers: 740 against 435), and one where two would leave half
-// the units idle (9 rows, 4 fp4 matrices of 1000 x 640: 6.2 against 7.6; 42 rows,
-// 2 int4 matrices of 4648 x 3328: 20 against 47).
+// rows each of 32 int4 experts of 7168 x 2048, a layer: 317 us against 369 with
+// 32 rows at a time, which read half the weights twice; 8 bf16 experts of 4096 x
+// 1408 with three rows each, where 25 were possible: 67 against 64), 16 where no
+// more can come or are likely.  Weight rows: two tiles a wave, or one where two
+// would leave half the units idle (9 rows, 4 fp4 matrices of 1000 x 640: 5.6
+// against 6.6; 42 rows, 2 int4 matrices of 4648 x 3328: 20 against 47).  Four for
+// bf16 win on some sizes (48 rows, 8 matrices of 7168 x 2048: 42 us against 47)
+// and lose on more (24 rows, 4 of 14336 x 4096: 98 against 89; 100 rows, 16 of
+// 4096 x 2048: 62 against 53; a layer of 97 tokens, 22 experts of 6680 x 2040: 485
+// against 449), with no rule on sizes to tell them apart.
 template <int KIND, int OUT>
 hipError_t wide_variant(const FewArgs& a, hipStream_t s) {
-  constexpr int half = OUT == kOutGated ? 2 : 1;       // a gate and an up tile an output tile
   const int average = (a.slots + a.experts - 1) / a.experts;
   const int mt = a.rows <= 16 * a.per_token || average <= 12 ? 1
                  : average < 28 ? 2 : 3;
   if (mt == 3) return launch_wide<KIND, 2, 3, OUT>(a, s);
-  if constexpr (kIsBf16<KIND>) {
-    if (groups_of(a, 4 / half * 64) >= kCus * 3 / 4)
-      return mt == 1 ? launch_wide<KIND, 4, 1, OUT>(a, s) : launch_wide<KIND, 4, 2, OUT>(a, s);
-  }
   if constexpr (OUT != kOutGated) {
     if (groups_of(a, 128) < kCus / 2)
       return mt == 1 ? launch_wide<KIND, 1, 1, OUT>(a, s) : launch_wide<KIND, 1, 2, OUT>(a, s);
@@ -1013,8 +1009,8 @@ hipError_t launch_thin(const FewArgs& a, hipStream_t s) {
 }
 
 // The thin form: four waves a workgroup, or eight where few workgroups have
-// long rows (one row, int4 4096 x 7168, 256 workgroups: 8.0 against 9.4 us;
-// one token through 8 fp4 experts, 1024 workgroups: 33 against 28).
+// long rows (one row, int4 4096 x 7168, 256 workgroups: 7.8 against 8.6 us;
+// one token through 8 fp4 experts, 1024 workgroups, the layer: 53 against 49).
 template <int KIND, int OUT>
 hipError_t thin_variant(const FewArgs& a, hipStream_t s) {
   if (groups_of(a, 16) <= 2 * kCus && a.K >= 4096) return launch_thin<KIND, OUT, 8>(a, s);
@@ -1045,7 +1041,8 @@ hipError_t rows_variant(const FewArgs& a, hipStream_t s) {
 
 // The joined down products: 32 channels a workgroup for 4-bit weights if that
 // leaves enough workgroups, else 16 (one token, 8 fp4 experts
-// of 7168 x 2048: 19.9 against 22.5 us; bf16, 512 x 256: 7.3 against 5.8).
+// of 7168 x 2048, the layer: 49 against 52 us; 3 tokens, bf16, 512 x 256: 11.8
+// against 10.2).
 template <int KIND, int NT>
 hipError_t launch_down(const DownArgs& a, hipStream_t s) {
   constexpr int C = NT * 16;
@@ -1079,16 +1076,17 @@ hipError_t with_kind(WeightKind kind, Fn fn) {
 }  // namespace
 
 // Whether bf16 matrices are read with the non-temporal hint: rows of whole
-// 128-byte lines, and more of them than the last-level cache (256 MB) could
-// hold beside anything else.  With both, 48 rows of 8 matrices of 7168 x 2048
-// took 48.8 against 52.3 us; rows that start inside a line fetch it twice under
-// the hint (a layer of 7160 channels: 161 against 148 us), and 40 MB of
-// matrices stay in the cache without it (14.7 against 21.7).  The 4-bit
-// formats gain 4 % at most and are read plainly.
+// 128-byte lines, and 64 MB of them or more, of which little would stay in the
+// last-level cache (256 MB) beside anything else.  With both, 48 rows of 8
+// matrices of 7168 x 2048 take 47 against 53 us, of 3584 x 2048 (117 MB) 27.6
+// against 29.6; rows that start inside a line fetch it twice under the
+// hint (8 matrices of 7160 x 7160: 183 against 159 us), and 42 MB of matrices
+// read again and again stay in the cache without it (20.5 against 19.7 in a
+// graph).  4-bit weights are read plainly.
 WeightKind stream_kind(const Weights& w, int experts, int rows, int K) {
   if (w.kind != kWBf16) return w.kind;
   const int64_t bytes = int64_t(experts) * rows * K * 2;
-  return K % 64 == 0 && reinterpret_cast<uintptr_t>(w.q) % 128 == 0 && bytes >= (128 << 20)
+  return K % 64 == 0 && reinterpret_cast<uintptr_t>(w.q) % 128 == 0 && bytes >= (64 << 20)
              ? kWBf16Stream
              : kWBf16;
 }
