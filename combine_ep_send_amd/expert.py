@@ -55,6 +55,16 @@ Weights = Union[torch.Tensor, W4Weights]
 # the named checks for its message.  The raw handle of the current stream costs
 # a thirtieth of torch.cuda.current_stream() (0.1 against 2.9 us).
 
+_INT_MAX = 0x7fffffff
+
+
+def _int(v: int, name: str) -> int:
+    # ctypes would drop the upper bits
+    if not -_INT_MAX <= v <= _INT_MAX:
+        raise ValueError(f"{name} = {v} is out of range")
+    return v
+
+
 def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
@@ -105,13 +115,17 @@ def _weights(w: Weights, name: str, index: int):
         if _first(q, f"{name}.q", _U8, 3) != index:
             raise ValueError(f"{name}.q is on {q.device}, not on cuda:{index}")
         E, N, half = q.shape
-        if group < 1:
-            raise ValueError(f"{name}.group must be positive")
+        if group not in (32, 64, 128):
+            raise ValueError(f"{name}.group must be 32, 64 or 128")
+        if max(E, N, half) > _INT_MAX // 2:
+            raise ValueError(f"{name} is too large: {tuple(q.shape)}")
         _on(scale, f"{name}.scale", _W4_SCALE[form], (E, N, 2 * half // group), index)
         return E, N, 2 * half, fmt, group, q.data_ptr(), scale.data_ptr()
     if _first(w, name, _BF16, 3) != index:
         raise ValueError(f"{name} is on {w.device}, not on cuda:{index}")
     E, N, K = w.shape
+    if max(E, N, K) > _INT_MAX:
+        raise ValueError(f"{name} is too large: {tuple(w.shape)}")
     return E, N, K, EP_W_BF16, 0, w.data_ptr(), None
 
 
@@ -128,9 +142,9 @@ def ep_quantize_w4(w: torch.Tensor, fmt: str = "int4", group: Optional[int] = No
     if _elsewhere(index, stream):
         return _there(ep_quantize_w4, index, stream, w, fmt, group, out=out)
     group = int(group) if group is not None else (32 if fmt == "fp4" else 128)
-    K = w.shape[-1]
-    if group < 1 or K < 1 or K % 128:
-        raise ValueError("K must be a multiple of 128 and group positive")
+    K = _int(w.shape[-1], "K")
+    if group not in (32, 64, 128) or K < 1 or K % 128:
+        raise ValueError("K must be a multiple of 128 and group 32, 64 or 128")
     qs, ss = (*w.shape[:-1], K // 2), (*w.shape[:-1], K // group)
     if out is None:
         out = W4Weights(w.new_empty(qs, dtype=_U8), w.new_empty(ss, dtype=_W4_SCALE[fmt]), fmt,
@@ -176,8 +190,10 @@ def ep_expert_matvec(x: torch.Tensor, weights: Weights, row_expert: Optional[tor
 @functools.lru_cache(maxsize=1024)
 def ep_moe_tokens_workspace_bytes(num_tokens: int, num_topk: int, hidden: int,
                                   inner: int) -> int:
-    return int(lib().ep_moe_tokens_workspace_bytes(int(num_tokens), int(num_topk), int(hidden),
-                                                   int(inner)))
+    sizes = [int(v) for v in (num_tokens, num_topk, hidden, inner)]
+    if max(map(abs, sizes)) > _INT_MAX:
+        return 0
+    return int(lib().ep_moe_tokens_workspace_bytes(*sizes))
 
 
 def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
@@ -201,7 +217,7 @@ def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.T
                       first_expert, bias=bias, out=out, workspace=workspace)
     T, H = x.shape
     _first(topk_idx, "topk_idx", _I64, 2)
-    K = topk_idx.shape[1]
+    K = _int(topk_idx.shape[1], "K")
     _on(topk_idx, "topk_idx", _I64, (T, K), index)
     _on(topk_weights, "topk_weights", _F32, (T, K), index)
     E, N13, K13, fmt13, group13, q13, scale13 = _weights(w13, "w13", index)
@@ -225,8 +241,9 @@ def ep_moe_tokens(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.T
     elif _first(workspace, "workspace", _U8, 1) != index:
         raise ValueError(f"workspace is on {workspace.device}, not on cuda:{index}")
     st = lib().ep_moe_tokens(
-        x.data_ptr(), topk_idx.data_ptr(), topk_weights.data_ptr(), T, K, H, I, int(first_expert),
-        E, fmt13, group13, q13, scale13, fmt2, group2, q2, scale2, b0, b1, out.data_ptr(),
+        x.data_ptr(), topk_idx.data_ptr(), topk_weights.data_ptr(), T, K, H, I,
+        _int(int(first_expert), "first_expert"), E, fmt13, group13, q13, scale13, fmt2, group2, q2,
+        scale2, b0, b1, out.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _raw_stream(index))
     if st != EP_OK:
         check(st, "ep_moe_tokens")
@@ -250,7 +267,7 @@ def ep_swiglu_fp8(gate_up: torch.Tensor, *, row_count: Optional[torch.Tensor] = 
     R, two = gate_up.shape
     if two % 256 or two == 0:
         raise ValueError("gate_up must be [R, 2I] with I a multiple of 128")
-    I = two // 2
+    I = _int(two // 2, "I")
     if row_count is not None:
         _on(row_count, "row_count", _I32, (1,), index)
     h = gate_up.new_empty((R, I)) if out is None else _on(out, "out", _BF16, (R, I), index)
@@ -278,7 +295,7 @@ def ep_swiglu_fp8_backward(dh: torch.Tensor, q: torch.Tensor, scale: torch.Tenso
         return _there(ep_swiglu_fp8_backward, index, stream, dh, q, scale, row_count=row_count,
                       recompute=recompute, out=out, h=h)
     R, I = dh.shape
-    if I % 128 or I == 0:
+    if _int(I, "I") % 128 or I == 0:
         raise ValueError("dh must be [R, I] with I a multiple of 128")
     _on(q, "q", _FP8, (R, 2 * I), index)
     _on(scale, "scale", _F32, (R, I // 64), index)
@@ -316,8 +333,9 @@ def ep_combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], token_row
         return _there(ep_combine_backward, index, stream, dout, y, token_row, topk_weights,
                       weight_grad=weight_grad, num_rows=num_rows, dy=dy, dw=dw)
     T, H = dout.shape
+    _int(H, "H")
     _first(token_row, "token_row", _I32, 2)
-    K = token_row.shape[1]
+    K = _int(token_row.shape[1], "K")
     _on(token_row, "token_row", _I32, (T, K), index)
     if topk_weights is not None:
         _on(topk_weights, "topk_weights", _F32, (T, K), index)

@@ -124,5 +124,7 @@ def test_python_refuses_host_tensors_and_wrong_types():
             call_()
     with pytest.raises(TypeError):
         ep.ep_expert_matvec(None, w)
+    assert ep.ep_moe_tokens_workspace_bytes((1 << 32) + 4, 2, 256, 128) == 0
+    assert ep.ep_moe_tokens_workspace_bytes(4, (1 << 32) + 2, 256, 128) == 0
     with pytest.raises(ValueError, match="fmt"):
         ep.ep_quantize_w4(w, "int8")

@@ -329,6 +329,24 @@ def test_refusals_on_the_device():
         lambda: ep.ep_combine_backward(x, None, ids.view(4, 1), None),
         lambda: ep.ep_combine_backward(x, x, ids.view(4, 1), None, num_rows=5),
     ]
+    big = 1 << 32                      # plus a size that would pass without it
+    none = x.new_zeros(0, big + 256)
+    bad += [
+        lambda: ep.ep_moe_tokens(x, idx, tw, w13, w2, big),
+        lambda: ep.ep_moe_tokens(x, idx, tw, w13, w2, -big),
+        lambda: ep.ep_moe_tokens(x[:0], idx.new_zeros(0, big + 2), tw.new_zeros(0, big + 2), w13,
+                                 w2),
+        lambda: ep.ep_quantize_w4(w, "int4", big + 32),
+        lambda: ep.ep_quantize_w4(w, "int4", 16),
+        lambda: ep.ep_quantize_w4(none),
+        lambda: ep.ep_expert_matvec(x, q._replace(group=big + 128), ids),
+        lambda: ep.ep_expert_matvec(x[:, :0].contiguous(), x.new_zeros(1, big + 1, 0)),
+        lambda: ep.ep_swiglu_fp8(x.new_zeros(0, 2 * big + 256)),
+        lambda: ep.ep_swiglu_fp8_backward(none, none.new_zeros(0, 2 * (big + 256)),
+                                          none.new_zeros(0, (big + 256) // 64)),
+        lambda: ep.ep_combine_backward(none, none, ids.view(4, 1)[:0], None),
+        lambda: ep.ep_combine_backward(x[:0], x, ids.new_zeros(0, big + 1), None),
+    ]
     for i, call in enumerate(bad):
         with pytest.raises(ValueError):
             call()
