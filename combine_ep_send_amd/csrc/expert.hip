@@ -110,28 +110,33 @@ __device__ __forceinline__ u32x4 decode_fp4(uint32_t d, float scale) {
                __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3)};
 }
 
-// Eight int4 codes c as the bf16 numbers 16 + c (exact: c in the top four
-// mantissa bits of 16), in the order 0 4 1 5 2 6 3 7.  c - 8 = (16 + c) - 24,
-// so the product with the row is this one's minus 24 times the row's sum,
-// which another matrix instruction gives for all the tiles of a block.
+// Eight int4 codes c as the bf16 numbers (c - 8) / 16, exact.  c ^ 8 is c - 8 in
+// two's complement, which a conversion instruction reads from the low four bits
+// of a byte; its fp32 result has the bf16 one in the upper half.  A zero weight
+// is a zero, so its channel drops out of the sum whatever its size, and a group
+// of 128 channels below 2^122 sums to less than 2^128.  (16 + c takes eight
+// operations instead of fourteen, but 24 times the row's sum has to come off
+// again, in products of its own: beside a large channel the others lose their
+// low bits, and sums leave fp32 earlier.  128 tokens, 32 experts of 7168 x 2048
+// in groups of 128, a layer, take 305 us this way and 323 that way; one matrix of
+// 7168 x 7168 in groups of 32 and 16 rows 26 and 24.)
 __device__ __forceinline__ u32x4 decode_int4(uint32_t d) {
-  uint32_t m = 0x00780078u, b = 0x41804180u;
-  // both constants in registers: mask and merge are then one instruction
-  asm("" : "+v"(m));
-  asm("" : "+s"(b));
-  return u32x4{((d << 3) & m) | b, ((d >> 1) & m) | b, ((d >> 5) & m) | b, ((d >> 9) & m) | b};
+  uint32_t lo = d ^ 0x88888888u;
+  uint32_t hi = lo >> 4;
+  asm("" : "+v"(lo), "+v"(hi));          // kept apart: the conversions then pick their bytes
+  u32x4 out;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = i ? (lo >> (8 * i)) & 0xFFu : lo, b = i ? (hi >> (8 * i)) & 0xFFu : hi;
+    out[i] = __builtin_amdgcn_perm(__float_as_uint(__builtin_amdgcn_cvt_off_f32_i4(int(b))),
+                                   __float_as_uint(__builtin_amdgcn_cvt_off_f32_i4(int(a))),
+                                   0x07060302u);
+  }
+  return out;
 }
-constexpr uint32_t kMinus24 = 0xC1C0C1C0u;
-
-// A row's eight channels in that order.
+// What a 1 of the accumulated sums stands for.
 template <int KIND>
-__device__ __forceinline__ u32x4 order_x(u32x4 x) {
-  if constexpr (!kIsInt4<KIND>) return x;
-  return u32x4{__builtin_amdgcn_perm(x.z, x.x, 0x05040100u),
-               __builtin_amdgcn_perm(x.z, x.x, 0x07060302u),
-               __builtin_amdgcn_perm(x.w, x.y, 0x05040100u),
-               __builtin_amdgcn_perm(x.w, x.y, 0x07060302u)};
-}
+constexpr float kUnit = kIsInt4<KIND> ? 16.0f : 1.0f;
 
 // ---------------------------------------------------------------------------
 // A stage of weights: NV 16-byte vectors a lane of each tile of 16 rows.
@@ -250,7 +255,7 @@ __device__ __forceinline__ void open_stage(Stage<KIND, NT, NV>& st, Scales<KIND,
 // Vector q's products into acc: MT tiles of 16 rows x against NT tiles of 16
 // weight rows.  A row x is the sum of XP bf16 rows.  x(mt, p, j): the fragment
 // of row tile mt, part p, for product j of the vector (bf16: the only one), as
-// order_x leaves it; use(mt): whether the tile has rows at all.
+// it lies in memory; use(mt): whether the tile has rows at all.
 template <int KIND, int NT, int NV, int MT, int XP, typename X, typename Use>
 __device__ __forceinline__ void vector_products(const Stage<KIND, NT, NV>& st,
                                                 const Scales<KIND, NT, NV>& scales, int q, X x,
@@ -290,41 +295,55 @@ __device__ __forceinline__ void vector_products(const Stage<KIND, NT, NV>& st,
   } else {
     constexpr int Q = KIND == kWInt4G128 ? 1 : KIND == kWInt4G64 ? 2 : 4;   // groups a vector
     constexpr int J = 4 / Q;                                                // products a group
-    const u32x4 minus = {kMinus24, kMinus24, kMinus24, kMinus24};
-    u32x4 b[NT][4];
+    u32x4 v[NT], b[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const u32x4 v = kSplit<KIND> ? st.v[nt][q] : transpose_groups(st.v[nt][q]);
+    for (int nt = 0; nt < NT; ++nt)
+      v[nt] = kSplit<KIND> ? st.v[nt][q] : transpose_groups(st.v[nt][q]);
+    auto decode = [&](int j) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[nt][j] = decode_int4(v[j]);
-    }
+      for (int nt = 0; nt < NT; ++nt) b[nt][j] = decode_int4(v[nt][j]);
+    };
+    auto products = [&](int mt, int i) {
+      u32x4 a[J][XP];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (!use(mt)) continue;
+      for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < Q; ++i) {
-        f32x4 base = {0.f, 0.f, 0.f, 0.f};
-        u32x4 a[J][XP];
+        for (int p = 0; p < XP; ++p) a[j][p] = x(mt, p, i * J + j);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-          for (int p = 0; p < XP; ++p) {
-            a[j][p] = x(mt, p, i * J + j);
-            base = mfma(a[j][p], minus, base);
-          }
+          for (int p = 0; p < XP; ++p) part = mfma(a[j][p], b[nt][i * J + j], part);
+        const uint32_t sw = i < 2 ? scales.s0[nt][q] : scales.s1[nt][q];
+        const float sc = Q > 1 && (i & 1) ? bf16_hi(sw) : bf16_lo(sw);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          f32x4 part = base;
+        for (int k = 0; k < 4; ++k) acc[mt][nt][k] = __builtin_fmaf(sc, part[k], acc[mt][nt][k]);
+      }
+    };
+    // Decoded all at once, one group's products cover the wait for another's (16
+    // rows of one 7168 x 7168 matrix in groups of 32: 26 us against 31.5); with
+    // eight or more fragments of x a vector the registers do not hold that (64
+    // tokens, 32 experts of 7168 x 2048 in groups of 32, a layer: 329 us group by
+    // group, 575 all at once).
+    if constexpr (Q * MT * XP < 8) {
 #pragma unroll
-          for (int j = 0; j < J; ++j)
+      for (int j = 0; j < 4; ++j) decode(j);
 #pragma unroll
-            for (int p = 0; p < XP; ++p) part = mfma(a[j][p], b[nt][i * J + j], part);
-          const uint32_t sw = i < 2 ? scales.s0[nt][q] : scales.s1[nt][q];
-          const float sc = Q > 1 && (i & 1) ? bf16_hi(sw) : bf16_lo(sw);
+      for (int mt = 0; mt < MT; ++mt) {
+        if (!use(mt)) continue;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            acc[mt][nt][k] = __builtin_fmaf(sc, part[k], acc[mt][nt][k]);
-        }
+        for (int i = 0; i < Q; ++i) products(mt, i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) decode(i * J + j);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          if (use(mt)) products(mt, i);
       }
     }
   }
@@ -384,7 +403,7 @@ __device__ __forceinline__ void own_tile(rsrc_t xr, uint32_t xoff, int plane, u3
 #pragma unroll
         for (int p = 0; p < XP; ++p)
           xs[((b * XP + p) * kFewRows + (lane >> 4)) * kXPitch<KIND> + (lane & 15)] =
-              order_x<KIND>(xb[d][b][p]);
+              xb[d][b][p];
       __builtin_amdgcn_wave_barrier();
       Scales<KIND, NT, NV> sc;
       open_stage<KIND, NT, NV>(w[d], sc);
@@ -581,7 +600,8 @@ __global__ __launch_bounds__(W * kWave) void few_thin_kernel(FewArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < kFewRows; ++k) red[wave][k][nt * 16 + lane] = acc[0][nt][k];
+        for (int k = 0; k < kFewRows; ++k)
+          red[wave][k][nt * 16 + lane] = kUnit<KIND> * acc[0][nt][k];
     }
     __syncthreads();
     const int mc = m - c0 < kFewRows ? m - c0 : kFewRows;
@@ -711,7 +731,7 @@ __global__ __launch_bounds__(kBlock, 2) void few_wide_kernel(FewArgs a) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int p = 0; p < XP; ++p) xs[buf][mt][p][frag][to] = order_x<KIND>(xb[d][mt][p][b]);
+            for (int p = 0; p < XP; ++p) xs[buf][mt][p][frag][to] = xb[d][mt][p][b];
           lds_barrier();
 #pragma unroll
           for (int q = b * (NV / XB); q < (b + 1) * (NV / XB); ++q)
@@ -743,12 +763,12 @@ __global__ __launch_bounds__(kBlock, 2) void few_wide_kernel(FewArgs a) {
           const int c = n0 + t * 16 + (lane & 15);
           if (c >= a.N) continue;
           if constexpr (OUT == kOutGated)
-            store_h(static_cast<__bf16*>(a.y) + slot * (2 * a.N) + c, a.N, acc[mt][t][i],
-                    acc[mt][C + t][i]);
+            store_h(static_cast<__bf16*>(a.y) + slot * (2 * a.N) + c, a.N,
+                    kUnit<KIND> * acc[mt][t][i], kUnit<KIND> * acc[mt][C + t][i]);
           else if constexpr (OUT == kOutBf16)
-            static_cast<__bf16*>(a.y)[slot * a.N + c] = __bf16(acc[mt][t][i]);
+            static_cast<__bf16*>(a.y)[slot * a.N + c] = __bf16(kUnit<KIND> * acc[mt][t][i]);
           else
-            static_cast<float*>(a.y)[slot * a.N + c] = acc[mt][t][i];
+            static_cast<float*>(a.y)[slot * a.N + c] = kUnit<KIND> * acc[mt][t][i];
         }
       }
   }
@@ -826,7 +846,8 @@ __global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a) {
           if (c0 + k < m)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              prod[(part * slots + order[f + c0 + k]) * C + nt * 16 + lane] = acc[0][nt][k];
+              prod[(part * slots + order[f + c0 + k]) * C + nt * 16 + lane] =
+                  kUnit<KIND> * acc[0][nt][k];
       }
     }
   }

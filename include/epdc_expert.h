@@ -81,9 +81,10 @@ int ep_quantize_w4(const void* w, int64_t num_rows, int channels, int weight_fmt
  * products and sums in fp32, rounded once.  The weights of an expert that
  * several rows name are read once for 4 to 48 of them, by the sizes.  Rows whose
  * id lies outside [0, E) get +0.
- * An int4 product computes sum (c + 16 - 24) x as a difference of two sums,
- * so that its x must stay below 2^122 in magnitude; an infinite or NaN
- * channel of a row gives that row NaN.
+ * An int4 product sums (c - 8) / 16 * x over a scale group in fp32 before the
+ * scale: with every channel below 2^122 in magnitude no such sum leaves fp32,
+ * whatever the codes and the group.  Larger finite channels may give infinities
+ * or NaN.
  *
  *   x           [num_rows, channels] bf16 in (16-byte aligned)
  *   row_expert  [num_rows] int32 in, or NULL when num_experts == 1 (all 0)
@@ -132,7 +133,8 @@ size_t ep_moe_tokens_workspace_bytes(int64_t num_tokens, int num_topk, int hidde
  *   workspace     ep_moe_tokens_workspace_bytes(T, K, H, I) bytes, 256-byte
  *                 aligned
  * H and I are multiples of 8 (of 128 where they are the channels of a 4-bit
- * matrix); the limits of ep_expert_matvec hold for both matrices.
+ * matrix); the limits of ep_expert_matvec hold for both matrices, that on the
+ * channels of an int4 product for x and for h.
  */
 int ep_moe_tokens(const void* x, const int64_t* topk_idx, const float* topk_weights,
                   int64_t num_tokens, int num_topk, int hidden, int inner, int first_expert,
