@@ -45,6 +45,14 @@ int check_weights(int fmt, int group, int out, int in, const void* w, const void
   return EP_OK;
 }
 
+// Whether a matrix [out, in], both within EPDC_FEW_CHANNELS (out: twice), has a
+// format that check_weights takes.
+bool some_format(int out, int in) {
+  if (out % 8 != 0 || in % 8 != 0) return false;
+  const int64_t channels = int64_t(out) * in;
+  return (in % 128 == 0 ? channels / 2 : channels * 2) <= EPDC_FEW_MATRIX_BYTES;
+}
+
 // The activations h in two bf16 parts, 256-byte aligned at their end.
 size_t h_bytes(size_t slots, int inner) { return (slots * size_t(inner) * 4 + 255) / 256 * 256; }
 
@@ -122,6 +130,7 @@ size_t ep_moe_tokens_workspace_bytes(int64_t num_tokens, int num_topk, int hidde
       num_tokens * num_topk > EPDC_FEW_SLOTS || hidden > EPDC_FEW_CHANNELS ||
       inner > EPDC_FEW_CHANNELS)
     return 0;
+  if (!some_format(2 * inner, hidden) || !some_format(hidden, inner)) return 0;
   const size_t slots = size_t(num_tokens) * size_t(num_topk);
   return kPlanBytes + h_bytes(slots, inner) +
          (few_down_joined(int(slots), hidden, inner) ? 0 : slots * size_t(hidden) * 4);

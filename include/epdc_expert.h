@@ -103,7 +103,8 @@ int ep_expert_matvec(const void* x, const int32_t* row_expert, int64_t num_rows,
  * Bytes of workspace ep_moe_tokens needs.  It holds the list of the experts in
  * use and the activations h; nothing in it has to be cleared, and nothing is
  * kept in it from one call to the next.  Calls that may overlap in time must
- * use different workspaces.  0 for sizes the call rejects.
+ * use different workspaces.  0 for sizes that the call rejects in every format
+ * of the weights.
  */
 size_t ep_moe_tokens_workspace_bytes(int64_t num_tokens, int num_topk, int hidden, int inner);
 

@@ -128,3 +128,24 @@ def test_python_refuses_host_tensors_and_wrong_types():
     assert ep.ep_moe_tokens_workspace_bytes(4, (1 << 32) + 2, 256, 128) == 0
     with pytest.raises(ValueError, match="fmt"):
         ep.ep_quantize_w4(w, "int8")
+
+
+def test_no_workspace_size_for_a_layer_that_is_refused():
+    """The size is 0 exactly where the call refuses the sizes in every format."""
+    L = _lib.lib()
+    size, layer = L.ep_moe_tokens_workspace_bytes, L.ep_moe_tokens
+
+    def refused(T, K, H, I):
+        """By every pair of formats, before the workspace is looked at."""
+        for f13, g13 in ((BF, 0), (INT4, 32), (FP4, 32)):
+            for f2, g2 in ((BF, 0), (INT4, 32), (FP4, 32)):
+                st = layer(A16, A16, A16, T, K, H, I, 0, 4, f13, g13, A16, A16, f2, g2, A16, A16,
+                           None, None, A16, None, 0, None)
+                assert st in (BAD, UNS, WS)
+                if st == WS:
+                    return False
+        return True
+    for H in (8, 12, 100, 104, 128, 7168, 32768, 65528, 65536, 65544):
+        for I in (4, 8, 12, 128, 200, 2048, 32760, 32768, 65535, 65536):
+            for T, K in ((1, 1), (128, 8)):
+                assert (size(T, K, H, I) == 0) == refused(T, K, H, I), (T, K, H, I)
