@@ -355,8 +355,6 @@ __device__ __forceinline__ void vector_products(const Stage<KIND, NT, NV>& st,
 // Rows past the fourth of a fragment repeat the four, and their products are
 // not used.  A wave's LDS accesses stay in order, so no barrier is needed.
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 4;
-
 // Blocks of 128 channels of x a stage needs.
 template <int KIND, int NV>
 constexpr int kXBlocks = kIsBf16<KIND> ? NV / 4 : NV;
@@ -533,9 +531,6 @@ __device__ __forceinline__ void store_h(__bf16* row, int64_t N, float g, float u
   row[0] = hi;
   row[N] = __bf16(finite ? v - float(hi) : 0.0f);
 }
-
-// What the first launch and the row call write.
-enum : int { kOutGated = 0, kOutBf16 = 1, kOutF32 = 2 };
 
 // Descriptors of expert e's matrix and its scales.
 template <int KIND>
@@ -786,7 +781,6 @@ __global__ __launch_bounds__(kBlock, 2) void few_wide_kernel(FewArgs a) {
 constexpr int kDownWaves = 8;
 constexpr int kDownBlock = kDownWaves * kWave;
 constexpr int kDownMaxSplit = 8;
-constexpr int kDownSlots = 64;                         // most slots
 
 template <int KIND, int NT, int NV, int D>
 __global__ __launch_bounds__(kDownBlock) void few_down_kernel(DownArgs a) {
@@ -974,96 +968,44 @@ __global__ __launch_bounds__(kBlock) void quantize_w4_kernel(QuantArgs a, int64_
   static_cast<uint32_t*>(a.q)[p] = code;
 }
 
-unsigned most_experts(const FewArgs& a) {
-  return unsigned(a.slots < a.experts ? a.slots : a.experts);
+FewSizes sizes_of(const FewArgs& a) {
+  return FewSizes{a.slots, a.rows, a.per_token, a.experts, a.N, a.K};
 }
-
-// Workgroups of a launch whose workgroups cover `channels` output channels.
-int64_t groups_of(const FewArgs& a, int channels) {
-  return int64_t((a.N + channels - 1) / channels) * most_experts(a);
-}
-
-constexpr int kCus = 256;
 
 template <int KIND, int NT, int MT, int OUT>
 hipError_t launch_wide(const FewArgs& a, hipStream_t s) {
   constexpr int C = (OUT == kOutGated ? NT / 2 : NT) * 16 * kWavesPerBlock;
   constexpr int NV = kIsBf16<KIND> ? 4 : 2;           // 256 bytes of a bf16 row, 128 of a 4-bit one
   constexpr int XP = OUT == kOutF32 ? 2 : 1;
-  const dim3 grid(unsigned((a.N + C - 1) / C), most_experts(a));
+  const dim3 grid(unsigned((a.N + C - 1) / C), unsigned(most_experts(sizes_of(a))));
   few_wide_kernel<KIND, NT, NV, MT, XP, OUT, 2><<<grid, kBlock, 0, s>>>(a);
   return hipGetLastError();
-}
-
-// The wide form's tiles.  Rows: an expert's rows are not known here, so the
-// average over the experts stands for them; 48 rows at a time from 28 on (32
-// rows each of 32 int4 experts of 7168 x 2048, a layer: 317 us against 369 with
-// 32 rows at a time, which read half the weights twice; 8 bf16 experts of 4096 x
-// 1408 with three rows each, where 25 were possible: 67 against 64), 16 where no
-// more can come or are likely.  Weight rows: two tiles a wave, or one where two
-// would leave half the units idle (9 rows, 4 fp4 matrices of 1000 x 640: 5.6
-// against 6.6; 42 rows, 2 int4 matrices of 4648 x 3328: 20 against 47).  Four for
-// bf16 win on some sizes (48 rows, 8 matrices of 7168 x 2048: 42 us against 47)
-// and lose on more (24 rows, 4 of 14336 x 4096: 98 against 89; 100 rows, 16 of
-// 4096 x 2048: 62 against 53; a layer of 97 tokens, 22 experts of 6680 x 2040: 485
-// against 449), with no rule on sizes to tell them apart.
-template <int KIND, int OUT>
-hipError_t wide_variant(const FewArgs& a, hipStream_t s) {
-  const int average = (a.slots + a.experts - 1) / a.experts;
-  const int mt = a.rows <= 16 * a.per_token || average <= 12 ? 1
-                 : average < 28 ? 2 : 3;
-  if (mt == 3) return launch_wide<KIND, 2, 3, OUT>(a, s);
-  if constexpr (OUT != kOutGated) {
-    if (groups_of(a, 128) < kCus / 2)
-      return mt == 1 ? launch_wide<KIND, 1, 1, OUT>(a, s) : launch_wide<KIND, 1, 2, OUT>(a, s);
-  }
-  return mt == 1 ? launch_wide<KIND, 2, 1, OUT>(a, s) : launch_wide<KIND, 2, 2, OUT>(a, s);
 }
 
 template <int KIND, int OUT, int W>
 hipError_t launch_thin(const FewArgs& a, hipStream_t s) {
   constexpr int NT = OUT == kOutGated ? 2 : 1;
   constexpr int NV = kIsBf16<KIND> ? 4 : 2;
-  const dim3 grid(unsigned((a.N + 15) / 16), most_experts(a));
+  const dim3 grid(unsigned((a.N + 15) / 16), unsigned(most_experts(sizes_of(a))));
   few_thin_kernel<KIND, NT, NV, W, OUT, 2><<<grid, W * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
-// The thin form: four waves a workgroup, or eight where few workgroups have
-// long rows (one row, int4 4096 x 7168, 256 workgroups: 7.8 against 8.6 us;
-// one token through 8 fp4 experts, 1024 workgroups, the layer: 53 against 49).
-template <int KIND, int OUT>
-hipError_t thin_variant(const FewArgs& a, hipStream_t s) {
-  if (groups_of(a, 16) <= 2 * kCus && a.K >= 4096) return launch_thin<KIND, OUT, 8>(a, s);
-  return launch_thin<KIND, OUT, 4>(a, s);
-}
-
-// Thin where an expert's rows come to one pass of four anyway, or where the
-// wide form would leave most of the chip idle; not where the channels are too
-// few for its four waves.  Thin against wide, whole calls in a graph: a layer of
-// 7 tokens, 27 bf16 experts of 3928 x 1408, 92 against 118 us; of 10 tokens, 26
-// of 5392 x 144, 26 against 51; 8 rows, 9 int4 matrices of 96 x 5760, 7.6
-// against 20.  The other way round: 76 rows, 9 bf16 matrices of 2040 x 3368, 54
-// against 42; a layer of 32 tokens, 29 int4 experts of 640 x 896, 45 against 27;
-// 8 rows, 10 bf16 matrices of 5632 x 232, 9.6 against 7.5.
-template <int KIND, int OUT>
-bool takes_thin(const FewArgs& a) {
-  if (a.rows <= kFewRows * a.per_token) return true;
-  if (a.K < (kIsBf16<KIND> ? 512 : 1024)) return false;
-  const int average = (a.slots + a.experts - 1) / a.experts;
-  const int64_t groups = groups_of(a, OUT == kOutGated ? 64 : 128);
-  return average <= 2 || (groups < 192 && average <= 6) || (groups < 48 && average <= 16);
-}
-
 template <int KIND, int OUT>
 hipError_t rows_variant(const FewArgs& a, hipStream_t s) {
-  return takes_thin<KIND, OUT>(a) ? thin_variant<KIND, OUT>(a, s) : wide_variant<KIND, OUT>(a, s);
+  const FewForm f = few_form(sizes_of(a), FewOut(OUT), kIsBf16<KIND>);
+  if (f.waves == 8) return launch_thin<KIND, OUT, 8>(a, s);
+  if (f.waves != 0) return launch_thin<KIND, OUT, 4>(a, s);
+  if constexpr (OUT != kOutGated) {
+    if (f.weight_tiles == 1)
+      return f.row_tiles == 1 ? launch_wide<KIND, 1, 1, OUT>(a, s)
+                              : launch_wide<KIND, 1, 2, OUT>(a, s);
+  }
+  if (f.row_tiles == 1) return launch_wide<KIND, 2, 1, OUT>(a, s);
+  if (f.row_tiles == 2) return launch_wide<KIND, 2, 2, OUT>(a, s);
+  return launch_wide<KIND, 2, 3, OUT>(a, s);
 }
 
-// The joined down products: 32 channels a workgroup for 4-bit weights if that
-// leaves enough workgroups, else 16 (one token, 8 fp4 experts
-// of 7168 x 2048, the layer: 49 against 52 us; 3 tokens, bf16, 512 x 256: 11.8
-// against 10.2).
 template <int KIND, int NT>
 hipError_t launch_down(const DownArgs& a, hipStream_t s) {
   constexpr int C = NT * 16;
@@ -1077,7 +1019,7 @@ hipError_t launch_down(const DownArgs& a, hipStream_t s) {
 template <int KIND>
 hipError_t down_variant(const DownArgs& a, hipStream_t s) {
   if constexpr (!kIsBf16<KIND>)
-    if (a.H >= 32 * kCus * 3 / 4) return launch_down<KIND, 2>(a, s);
+    if (down_tiles(a.H, false) == 2) return launch_down<KIND, 2>(a, s);
   return launch_down<KIND, 1>(a, s);
 }
 
@@ -1094,37 +1036,11 @@ hipError_t with_kind(WeightKind kind, Fn fn) {
   }
 }
 
-}  // namespace
-
-// Whether bf16 matrices are read with the non-temporal hint: rows of whole
-// 128-byte lines, and 64 MB of them or more, of which little would stay in the
-// last-level cache (256 MB) beside anything else.  With both, 48 rows of 8
-// matrices of 7168 x 2048 take 47 against 53 us, of 3584 x 2048 (117 MB) 27.6
-// against 29.6; rows that start inside a line fetch it twice under the
-// hint (8 matrices of 7160 x 7160: 183 against 159 us), and 42 MB of matrices
-// read again and again stay in the cache without it (20.5 against 19.7 in a
-// graph).  4-bit weights are read plainly.
 WeightKind stream_kind(const Weights& w, int experts, int rows, int K) {
-  if (w.kind != kWBf16) return w.kind;
-  const int64_t bytes = int64_t(experts) * rows * K * 2;
-  return K % 64 == 0 && reinterpret_cast<uintptr_t>(w.q) % 128 == 0 && bytes >= (64 << 20)
-             ? kWBf16Stream
-             : kWBf16;
+  return w.kind == kWBf16 && streams_bf16(w.q, experts, rows, K) ? kWBf16Stream : w.kind;
 }
 
-// Products and sum in one launch for a few slots (it saves a launch and y),
-// unless few output channels would make few workgroups, each of which reads its
-// rows of every expert: 5 tokens, 30 slots of 384 x 1664 int4 experts take 39 us
-// joined and 19 apart.  With more than 32 slots the wide form shares weights that
-// this one reads per pass, unless the products are too small for that to show: 64
-// slots of 13 fp4 experts of 3456 x 1664, 64 us joined and 52 apart; of 64 experts
-// of 7168 x 2048, 300 and 268; but 32 slots of 32 int4 experts of 4096 x 1024, 51
-// and 72; 18 slots of 15 bf16 experts of 4888 x 136, 17 and 20.  The price: with
-// most experts elsewhere, 42 slots of 5888 x 768, 25 joined and 27 apart.
-bool few_down_joined(int slots, int hidden, int inner) {
-  return (slots <= kDownSlots / 2 && hidden >= 2048) ||
-         (slots <= kDownSlots && slots * int64_t(inner) <= 8192);
-}
+}  // namespace
 
 hipError_t launch_few_rows(const FewArgs& a, bool gated, hipStream_t s) {
   return with_kind(stream_kind(a.w, a.experts, gated ? 2 * a.N : a.N, a.K), [&](auto kind) {

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "expert_rules.h"
+
 namespace epdc {
 
 constexpr int kFewSlots = 1024;    // slots (token, k) or rows of one call
@@ -69,9 +71,7 @@ struct DownArgs {
   void* out;
   float* y;                        // [slots, H], where the sum is a launch of its own
 };
-// Whether a layer of so many slots sums its down products in the launch that
-// makes them; otherwise they go through y in its workspace.
-bool few_down_joined(int slots, int hidden, int inner);
+// The products go through y in the workspace unless few_down_joined.
 hipError_t launch_few_down(const DownArgs& a, hipStream_t s);
 
 struct QuantArgs {
