@@ -35,10 +35,12 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 }
 
 // 1 / (1 + exp(-g)): exp on the hardware's base-2 exponential, relative error
-// about |g| * 2^-23, and a reciprocal within one unit in the last place.  Past
-// |g| = 88 the exponential is 0 or infinite and the result 1 or 0.
+// about |g| * 2^-23, and a reciprocal within one unit in the last place.  The
+// reciprocal instruction flushes results below 2^-126, so it takes a quarter of
+// the sum; the product with 1/4 keeps subnormals.  Past |g| = 88.7 the
+// exponential is 0 or infinite and the result 1 or 0.
 __device__ __forceinline__ float sigmoid(float g) {
-  return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+  return 0.25f * __builtin_amdgcn_rcpf(__builtin_fmaf(__expf(-g), 0.25f, 0.25f));
 }
 
 // e4m3 codes and scale of 128 channels held by 16 lanes, 8 each: scale =

@@ -276,3 +276,37 @@ def test_combine_backward_skips_rows_outside_the_buffer():
     check(dy[named], rdy[named], tdy[named])
     check(dw, rdw, tdw)
     assert (buf[[2, 3, 5]] == 7).all()
+
+
+def test_activation_where_the_sigmoid_is_subnormal():
+    """Gates of -87.5 to -88.5: 1 + exp(-g) lies past 2^126 and its reciprocal
+    below the normal numbers, but not the product with a large u or dh."""
+    R, I = 3, 128
+    gate = np.array([-87.5, -88.0, -88.5])[:, None] * np.ones((R, I))
+    rng = np.random.default_rng(11)
+    u = np.ldexp(rng.uniform(1, 2, (R, I)), 118)
+    gu = bf16(np.concatenate([gate, u], 1))
+    d = bf16(rng.uniform(1, 2, (R, I)))
+
+    def bound(g, value, factor):
+        # as product_bound, but for the step of a subnormal sigmoid: 2^-149 and a half,
+        # twice for the reciprocal's last place
+        return BF16 * np.abs(value) + 1.01 * np.abs(value) * (np.abs(g) + 8) * 2.0 ** -22 + \
+            np.abs(factor) * 2.0 ** -148
+    h, q, scale = ep.ep_swiglu_fp8(gu.to(DEV))
+    v = f64(gu)
+    g, u = v[:, :I], v[:, I:]
+    ref = g * sigmoid(g) * u
+    assert np.abs(ref).min() > 2.0 ** -5
+    check(h, ref, bound(g, ref, g * u), "h")
+    dgu, again = ep.ep_swiglu_fp8_backward(d.to(DEV), q, scale)
+    kept = q.float().cpu().double().numpy() * \
+        np.repeat(scale.cpu().double().numpy(), 128, -1)
+    # the values fp32 makes of code * scale
+    kept = kept.astype(np.float32).astype(np.float64)
+    g, u, d = kept[:, :I], kept[:, I:], f64(d)
+    s = sigmoid(g)
+    check(again, g * s * u, bound(g, g * s * u, g * u), "h again")
+    dg, du = d * u * s * (1 + g * (1 - s)), d * g * s
+    check(dgu[:, :I], dg, bound(g, dg, d * u * g), "dg")
+    check(dgu[:, I:], du, bound(g, du, d * g) + TINY, "du")
