@@ -520,14 +520,16 @@ __device__ __forceinline__ void write_plan(const SharedPlan& sp, const FewArgs& 
   for (int i = threadIdx.x; i < m; i += BLOCK) a.plan->order[first + i] = sp.list[i];
 }
 
-// h = silu(g) * u in two bf16 parts, 16 significant bits together: bf16 alone
-// would double the squared error of the layer's output.  The first part is
-// cut, not rounded, so that it stays finite where h is.
+// h = silu(g) * u in two bf16 parts, off by at most 2^-17 of it: bf16 alone would
+// double the squared error of the layer's output, a third part would take half
+// as many products again.  The first part is rounded (cut, it would leave 2^-16),
+// but cut where rounding would make it infinite.
 __device__ __forceinline__ void store_h(__bf16* row, int64_t N, float g, float u) {
   const float v = g / (1.0f + __expf(-g)) * u;
   const bool finite = __builtin_fabsf(v) < __builtin_inff();
-  const __bf16 hi =
-      finite ? __bf16(__uint_as_float(__float_as_uint(v) & 0xFFFF0000u)) : __bf16(v);
+  __bf16 hi = __bf16(v);
+  if (finite && __builtin_fabsf(float(hi)) == __builtin_inff())
+    hi = __bf16(__uint_as_float(__float_as_uint(v) & 0xFFFF0000u));
   row[0] = hi;
   row[N] = __bf16(finite ? v - float(hi) : 0.0f);
 }

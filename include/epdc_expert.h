@@ -118,9 +118,9 @@ size_t ep_moe_tokens_workspace_bytes(int64_t num_tokens, int num_topk, int hidde
  * output is multiplied by its weight in fp32 and added in ascending k from
  * +0.0, the biases that are given after it, bias0 first, as in ep_combine, but
  * without the rounding of a slot's output to bf16.  h is carried as the sum of
- * two bf16 numbers (16 significant bits).  Slots of other ids (-1, or another
- * GPU's experts) are skipped; a token with no local slot gives +0 plus the
- * biases.
+ * two bf16 numbers (off by at most 2^-17 of it).  Slots of other ids (-1, or
+ * another GPU's experts) are skipped; a token with no local slot gives +0 plus
+ * the biases.
  * The result does not depend on the order in which workgroups run.
  *
  *   x             [T,H] bf16 in (16-byte aligned)

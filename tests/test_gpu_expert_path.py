@@ -352,3 +352,43 @@ def test_refusals_on_the_device():
             call()
             print("accepted:", i, flush=True)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,K", [(1, 1), (4, 2), (20, 2), (40, 2), (70, 2)])
+def test_layer_carries_h_within_two_to_the_minus_17(T, K):
+    """One-hot rows make h = g * u of 24 bits exactly, an identity as the second
+    matrix and minus bf16(h) as the bias leave what bf16 does not hold of h."""
+    rng = np.random.default_rng(T)
+    E, H, I = 2, 256, 256
+    w13 = np.zeros((E, 2 * I, H))
+    a, b, g = rng.integers(128, 256, (3, E, I))
+    w13[:, :I, 0], w13[:, I:, 1], w13[:, I:, 2] = g, a, b      # exp(-128) adds nothing to 1
+    h = g * (a + b * 2.0 ** -8)
+    assert (h.astype(np.float32) == h).all()
+    x = np.zeros((T, H))
+    x[:, 0], x[:, 1], x[:, 2] = 1, 1, 2.0 ** -8
+    idx = np.full((T, K), -1, np.int64)
+    idx[:, 0] = rng.integers(0, E, T)
+    w = np.ones((T, K), np.float32)
+    near = f64(bf16(h))
+    out = ep.ep_moe_tokens(bf16(x).to(DEV), torch.from_numpy(idx).to(DEV), torch.from_numpy(w).to(DEV),
+                           bf16(w13).to(DEV), bf16(np.broadcast_to(np.eye(H), (E, H, I))).to(DEV),
+                           bias=bf16(-near[idx[:, 0]]).to(DEV))
+    rest = (h - near)[idx[:, 0]]
+    check(out, rest, 2.0 ** -17 * h[idx[:, 0]] + BF16 * np.abs(f64(out.cpu())))
+
+
+def test_layer_keeps_h_finite_up_to_the_largest_number():
+    """h of all 24 bits set just below 2^128, where rounding to bf16 overflows."""
+    H = I = 128
+    w13 = np.zeros((1, 2 * I, H))
+    w13[0, :I, 0], w13[0, I:, 1], w13[0, I:, 2] = 128, 255, 255
+    top = 128 * (255 + 255 * 2.0 ** -8)
+    x = np.zeros((1, H))
+    x[0, :3] = 1, 2.0 ** 113, 2.0 ** 105
+    w2 = np.eye(H)[None] * 2.0 ** -60
+    out = ep.ep_moe_tokens(bf16(x).to(DEV), torch.zeros(1, 1, dtype=torch.int64, device=DEV),
+                           torch.ones(1, 1, device=DEV), bf16(w13).to(DEV), bf16(w2).to(DEV))
+    ref = np.full((1, H), top * 2.0 ** 53)
+    assert top * 2.0 ** 113 < 2.0 ** 128
+    check(out, ref, (BF16 + 2.0 ** -15) * ref)
