@@ -322,12 +322,13 @@ __device__ __forceinline__ void vector_products(const Stage<KIND, NT, NV>& st,
         for (int k = 0; k < 4; ++k) acc[mt][nt][k] = __builtin_fmaf(sc, part[k], acc[mt][nt][k]);
       }
     };
-    // Decoded all at once, one group's products cover the wait for another's (16
-    // rows of one 7168 x 7168 matrix in groups of 32: 26 us against 31.5); with
-    // eight or more fragments of x a vector the registers do not hold that (64
-    // tokens, 32 experts of 7168 x 2048 in groups of 32, a layer: 329 us group by
-    // group, 575 all at once).
-    if constexpr (Q * MT * XP < 8) {
+    // Decoded all at once, one group's products cover the wait for another's (42
+    // rows, 2 matrices of 4608 x 3328 in groups of 32, one weight tile a wave: 19
+    // us against 24 group by group; 16 rows of one of 7168 x 7168: 26.5 against
+    // 31.5).  The registers do not hold that for two weight tiles and eight or
+    // more fragments of x a vector (64 tokens, 32 experts of 7168 x 2048 in groups
+    // of 32, a layer: 323 us group by group, 575 all at once).
+    if constexpr (NT == 1 || Q * MT * XP < 8) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) decode(j);
 #pragma unroll
