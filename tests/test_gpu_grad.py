@@ -310,3 +310,16 @@ def test_activation_where_the_sigmoid_is_subnormal():
     dg, du = d * u * s * (1 + g * (1 - s)), d * g * s
     check(dgu[:, :I], dg, bound(g, dg, d * u * g), "dg")
     check(dgu[:, I:], du, bound(g, du, d * g) + TINY, "du")
+
+
+def test_checkpoint_scale_is_pytorchs_quotient_on_the_gpu():
+    """amax / 448.0 of a GPU tensor, which PyTorch computes as a product with
+    the reciprocal: the same bits, over every exponent of bf16."""
+    v = torch.arange(1, 0x7F80, dtype=torch.int16)                 # every positive finite value
+    v = torch.cat([v, v[:128 * 256 - len(v)]]).view(torch.bfloat16).to(DEV)
+    gu = torch.zeros(128, 2 * 16384, dtype=torch.bfloat16, device=DEV)
+    gu[:, ::128] = v.view(128, 256)
+    gu[:, 5::128] = -v.view(128, 256) / 2
+    _, _, scale = ep.ep_swiglu_fp8(gu)
+    amax = gu.float().view(128, 256, 128).abs().amax(-1)
+    assert torch.equal(scale.view(torch.int32), (amax / 448.0).view(torch.int32))
