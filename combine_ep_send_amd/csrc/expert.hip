@@ -555,7 +555,9 @@ __device__ __forceinline__ rsrc_t scale_rsrc(const Weights& w, int e, int rows, 
 // up through LDS in a fixed order.  kOutGated: a tile is half gate and half up
 // rows.  Bound by the weights and, under 10 us, by the launch and the first
 // loads: the gate and up rows of 8 fp4 experts of 7168 x 2048 for one token, 125
-// MB, 30 us (4.2 TB/s); one row, int4 4096 x 7168, 15 MB, 8.2 us.
+// MB, 30 us (4.2 TB/s); one row, int4 4096 x 7168, 15 MB, 8.2 us, of which the
+// waves wait for 56 %: each has three or four stages, two rounds of loads one
+// after the other, and the first starts after find_expert.
 // ---------------------------------------------------------------------------
 template <int KIND, int NT, int NV, int W, int OUT, int D>
 __global__ __launch_bounds__(W * kWave) void few_thin_kernel(FewArgs a) {
@@ -635,10 +637,15 @@ __device__ __forceinline__ void lds_barrier() {
 // rows and share the rows x, which each fetches its part of and passes on
 // through LDS, stage by stage.  A row x then comes out of the L2 once for
 // 64*NT weight rows.  bf16 is bound by the weights: 48 rows, 8 matrices of 7168
-// x 2048, 235 MB, 47 us (5.0 TB/s) a call.  32 rows for each of 32 int4 experts of
-// 7168 x 2048 take 194 us (gate and up; 137 with the loads alone, 79 with the
-// decoding and products alone) and 173 us (down; 104 and 77): the two overlap
-// only partly, as the registers allow two waves a SIMD.
+// x 2048, 235 MB, 45 us (5.2 TB/s) a call.  32 rows for each of 32 int4 experts of
+// 7168 x 2048 take 192 us (gate and up) and 165 us (down): at a vector instruction
+// per four cycles and a matrix instruction per sixteen, the former would take 71
+// and 43 us alone, the latter 29 and 29.  The waves wait for memory, LDS and
+// barriers 28 and 39 % of their time: the registers allow two waves a SIMD, which
+// do not cover it.  Eight instances spill registers to scratch memory (int4 in
+// groups of 32 with two weight tiles and two or three row tiles, 9 to 32, in the
+// down product 29 and 65; in groups of 64 and 128 the down product with three
+// row tiles, 6 and 8: 15 of the 44 MB that the down product above writes).
 // ---------------------------------------------------------------------------
 template <int KIND, int NT, int NV, int MT, int XP, int OUT, int D>
 __global__ __launch_bounds__(kBlock, 2) void few_wide_kernel(FewArgs a) {
@@ -897,10 +904,13 @@ __global__ __launch_bounds__(kBlock) void few_sum_kernel(DownArgs a) {
 
 // ---------------------------------------------------------------------------
 // bf16 rows to 4-bit codes and scales.  A lane takes 8 channels (16 bytes in,
-// 4 out); the group/8 lanes of a group share its largest magnitude.  The exact
-// divisions and the choice of the code bound it, not memory: 65536 x 7168 take
-// 385 us as int4 in groups of 128 (3.1 TB/s), 378 us as fp4.  Weights pass here
-// once, so it stays simple.
+// 4 out); the group/8 lanes of a group share its largest magnitude.  Vector
+// instructions bound it, not memory: 237 a wave for int4 (nine exact divisions),
+// 245 for fp4 (the choice of the code, with as many scalar ones for its
+// branches), in both a 64-bit division for the group's index.  65536 x 7168 take
+// 376 us as int4 in groups of 128 (3.1 TB/s), 379 us as fp4; at one instruction
+// per four cycles those alone take 350 and 370.  Weights pass here once, so it
+// stays simple.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t e2m1_code(float v) {
   // nearest of 0 .5 1 1.5 2 3 4 6, ties to the even code

@@ -139,8 +139,8 @@ def combine_backward(dout: torch.Tensor, local_out: torch.Tensor, handle: Dispat
                      weighted: bool = True, d_local_out: Optional[torch.Tensor] = None):
     """Gradient of ``combine``: (d_local_out, shaped as local_out; the top-k
     weights' gradient [T,K] fp32, None unweighted).  Rows past the layout's
-    pairs are left as they are in a ``d_local_out`` that is passed, zero in one
-    allocated here."""
+    pairs are left as they are in a ``d_local_out`` that is passed (with what a
+    longer layout left there), zero in one allocated here."""
     return ep_combine_backward(dout, local_out, handle.token_row,
                                handle.topk_weights if weighted else None, dy=d_local_out)
 

@@ -5,8 +5,10 @@ gated activation with its 8-bit checkpoint, and the gradient of the combine.
 As in ``ops``, the functions mirror the C entry points: they check dtypes,
 shapes and devices, allocate outputs the caller did not pass, and enqueue on
 the current (or given) HIP stream.  They run on the device of their tensors,
-whichever is current.  They record nothing for autograd; the backward passes
-are calls of their own."""
+whichever is current.  They record nothing for autograd: outputs
+do not require gradients even where an input does, without an error or a
+warning.  The backward passes are calls of their own, to be made by hand or
+from a ``torch.autograd.Function``."""
 
 from __future__ import annotations
 
@@ -326,8 +328,8 @@ def ep_combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], token_row
     dw[t, k] = <dout[t], y[token_row[t, k]]>.  With ``topk_weights=None`` (the
     unweighted combine) or ``weight_grad=False`` dw is None and y is not read:
     it may then be None, with ``num_rows`` or ``dy`` giving the rows.  Rows no
-    slot names are left as they are in ``dy``; a result allocated here has
-    zeros there.  The gradient of a combine's bias is dout itself."""
+    slot names are left as they are in ``dy``, with what an earlier layout left
+    there; a result allocated here has zeros.  The gradient of a combine's bias is dout itself."""
     index = _first(dout, "dout", _BF16, 2)
     if _elsewhere(index, stream):
         return _there(ep_combine_backward, index, stream, dout, y, token_row, topk_weights,

@@ -153,7 +153,8 @@ int ep_moe_tokens(const void* x, const int64_t* topk_idx, const float* topk_weig
  *              e4m3(fp32(x / scale)).
  * The rounding of the codes, zeros, NaN and infinities follow
  * ep_dispatch_permute's fp8 form, whose scale is fp32(amax / 448), at most one
- * unit in the last place from this one.  A user keeps q and scale (2I + I/16
+ * unit in the last place from this one.  The product is what PyTorch computes
+ * for amax / 448.0 on the GPU, so that q and scale equal a checkpoint made there.  A user keeps q and scale (2I + I/16
  * bytes a row) instead of gate_up and h (6I bytes).
  *
  *   gate_up    [num_rows, 2I] bf16 in (16-byte aligned)
@@ -191,10 +192,11 @@ int ep_swiglu_fp8_backward(const void* dh, const void* q, const float* scale, in
  *   dw[t,k] = <dout[t,:], y[token_row[t,k],:]> in fp32, 0 for slots with no
  *             row.
  * The sums run in a fixed order.  The gradient of a bias is dout itself.
- * Rows that no slot names (padding, spare capacity) are left as they are, so
- * a caller who reads those clears them once.  The slots of two tokens must
- * not name the same row (no layout of epdc.h does).  The gradient of the
- * dispatch is ep_combine with topk_weights == NULL.
+ * Rows that no slot names (padding, spare capacity) are left as they are: a
+ * caller who reads those clears them, and again for every new token_row, since
+ * a row that a slot named before may be one that none names now.  The slots of
+ * two tokens must not name the same row (no layout of epdc.h does).  The
+ * gradient of the dispatch is ep_combine with topk_weights == NULL.
  *
  *   dout          [T,H] bf16 in (16-byte aligned)
  *   y             [num_rows,H] bf16 in (16-byte aligned); may be NULL when dw
