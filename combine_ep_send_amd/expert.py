@@ -329,7 +329,11 @@ def ep_combine_backward(dout: torch.Tensor, y: Optional[torch.Tensor], token_row
     unweighted combine) or ``weight_grad=False`` dw is None and y is not read:
     it may then be None, with ``num_rows`` or ``dy`` giving the rows.  Rows no
     slot names are left as they are in ``dy``, with what an earlier layout left
-    there; a result allocated here has zeros.  The gradient of a combine's bias is dout itself."""
+    there; a result allocated here has zeros.  The gradient of a combine's bias is dout itself.
+
+    With a regroup's ``row_map`` and the received rows' weights in place of
+    ``token_row`` and ``topk_weights`` it is the gradient of restore_by_expert;
+    that of permute_by_expert is ``ep_combine(d_perm_x, row_map, None)``."""
     index = _first(dout, "dout", _BF16, 2)
     if _elsewhere(index, stream):
         return _there(ep_combine_backward, index, stream, dout, y, token_row, topk_weights,

@@ -196,7 +196,10 @@ int ep_swiglu_fp8_backward(const void* dh, const void* q, const float* scale, in
  * caller who reads those clears them, and again for every new token_row, since
  * a row that a slot named before may be one that none names now.  The slots of
  * two tokens must not name the same row (no layout of epdc.h does).  The
- * gradient of the dispatch is ep_combine with topk_weights == NULL.
+ * gradient of the dispatch is ep_combine with topk_weights == NULL.  The way
+ * back from the expert-major rows of ep_regroup_by_expert is ep_combine over its
+ * row_map, so that its gradient is this call with token_row = row_map, and the
+ * regroup's is ep_combine over row_map with topk_weights == NULL.
  *
  *   dout          [T,H] bf16 in (16-byte aligned)
  *   y             [num_rows,H] bf16 in (16-byte aligned); may be NULL when dw
