@@ -154,8 +154,9 @@ int ep_moe_tokens(const void* x, const int64_t* topk_idx, const float* topk_weig
  * The rounding of the codes, zeros, NaN and infinities follow
  * ep_dispatch_permute's fp8 form, whose scale is fp32(amax / 448), at most one
  * unit in the last place from this one.  The product is what PyTorch computes
- * for amax / 448.0 on the GPU, so that q and scale equal a checkpoint made there.  A user keeps q and scale (2I + I/16
- * bytes a row) instead of gate_up and h (6I bytes).
+ * for amax / 448.0 on the GPU, so that q and scale equal a checkpoint made
+ * there.  A user keeps q and scale (2I + I/16 bytes a row) instead of gate_up
+ * and h (6I bytes).
  *
  *   gate_up    [num_rows, 2I] bf16 in (16-byte aligned)
  *   row_count  [1] int32 in, device memory, or NULL: rows from row_count[0] on
