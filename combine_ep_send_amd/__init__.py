@@ -5,6 +5,8 @@
 ``ep_dispatch_permute``, ``ep_batched_prepare``, ``ep_combine``);
 ``expert`` that of ``include/epdc_expert.h``, the expert side
 (``ep_moe_tokens``, ``ep_expert_matvec``, ``ep_swiglu_fp8`` ...);
+``router`` that of ``include/epdc_router.h``, what runs before the dispatch
+(``ep_rms_norm``, ``ep_router_logits``, ``ep_route`` ...);
 ``dispatch`` holds the dispatcher-level functions (``dispatch``,
 ``combine``, ``dispatch_chunked_forward``, ``batched_prepare`` ...).
 Importing the package does not load the library; the first call does, and
@@ -38,6 +40,19 @@ from .expert import (  # noqa: F401
     ep_quantize_w4,
     ep_swiglu_fp8,
     ep_swiglu_fp8_backward,
+)
+from .router import (  # noqa: F401
+    RmsNorm,
+    ep_dispatch_permute_quantized,
+    ep_rms_norm,
+    ep_rms_norm_backward,
+    ep_rms_norm_backward_workspace_bytes,
+    ep_route,
+    ep_route_backward,
+    ep_router_logits,
+    ep_router_logits_backward,
+    ep_router_logits_backward_workspace_bytes,
+    ep_router_logits_workspace_bytes,
 )
 from .ops import (  # noqa: F401
     Counts,

@@ -10,6 +10,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libepdc.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "epdc.h")
 EXPERT_HEADER = os.path.join(os.path.dirname(PKG), "include", "epdc_expert.h")
+ROUTER_HEADER = os.path.join(os.path.dirname(PKG), "include", "epdc_router.h")
 
 EP_OK = 0
 EP_ERR_INVALID_ARG = -1
@@ -26,11 +27,16 @@ EP_SCALE_UE8M0 = 2
 EP_W_BF16 = 0
 EP_W_INT4 = 1
 EP_W_FP4 = 2
+EP_NORM_W_BF16 = 0
+EP_NORM_W_F32 = 1
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 _SIGNATURES = {
     "ep_abi_version": (_I32, []),
@@ -81,6 +87,25 @@ _EXPERT_SIGNATURES = {
     "ep_combine_backward": (_I32, [_P, _P, _I64, _P, _P, _I64, _I32, _I32, _P, _P, _P]),
 }
 
+# include/epdc_router.h
+_ROUTER_SIGNATURES = {
+    "ep_router_abi_version": (_I32, []),
+    "ep_rms_norm": (_I32, [_P, _P, _P, _I32, _I64, _I32, _F, _P, _P, _P, _P, _I32, _P, _P]),
+    "ep_rms_norm_backward_workspace_bytes": (_SZ, [_I64, _I32]),
+    "ep_rms_norm_backward": (
+        _I32, [_P, _P, _P, _I32, _P, _P, _I64, _I32, _P, _P, _P, _SZ, _P]),
+    "ep_router_logits_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "ep_router_logits": (_I32, [_P, _P, _I64, _I32, _I32, _P, _P, _SZ, _P]),
+    "ep_router_logits_backward_workspace_bytes": (_SZ, [_I64, _I32, _I32]),
+    "ep_router_logits_backward": (
+        _I32, [_P, _P, _P, _I64, _I32, _I32, _P, _P, _P, _SZ, _P]),
+    "ep_route": (
+        _I32, [_P, _I64, _I32, _I32, _I32, _P, _I32, _I32, _I32, _I32, _F, _P, _P, _P, _P]),
+    "ep_route_backward": (_I32, [_P, _P, _P, _I64, _I32, _I32, _I32, _I32, _F, _P, _P]),
+    "ep_dispatch_permute_quantized": (
+        _I32, [_P, _P, _I32, _I64, _I32, _P, _I32, _I64, _P, _P, _P]),
+}
+
 _lib = None
 
 
@@ -88,6 +113,8 @@ _lib = None
 ABI_VERSION = 6
 # EPDC_EXPERT_ABI_VERSION of include/epdc_expert.h
 EXPERT_ABI_VERSION = 1
+# EPDC_ROUTER_ABI_VERSION of include/epdc_router.h
+ROUTER_ABI_VERSION = 1
 
 
 def header_functions(path=HEADER):
@@ -128,7 +155,18 @@ def lib():
             raise ImportError(
                 f"{LIB_PATH} reports expert ABI version {ver()}, these bindings are for "
                 f"{EXPERT_ABI_VERSION}: rebuild it with `python -m combine_ep_send_amd.build`")
-        for name, (res, args) in {**_SIGNATURES, **_EXPERT_SIGNATURES}.items():
+        try:
+            ver = L.ep_router_abi_version
+        except AttributeError:
+            raise ImportError(f"{LIB_PATH} lacks the calls before the dispatch: rebuild it with "
+                              "`python -m combine_ep_send_amd.build`")
+        ver.restype, ver.argtypes = _I32, []
+        if ver() != ROUTER_ABI_VERSION:
+            raise ImportError(
+                f"{LIB_PATH} reports router ABI version {ver()}, these bindings are for "
+                f"{ROUTER_ABI_VERSION}: rebuild it with `python -m combine_ep_send_amd.build`")
+        for name, (res, args) in {**_SIGNATURES, **_EXPERT_SIGNATURES,
+                                  **_ROUTER_SIGNATURES}.items():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args

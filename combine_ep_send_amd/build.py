@@ -20,7 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libepdc.so")
 SOURCES = ["scan.hip", "fused.hip", "rows.hip", "api.hip", "expert.hip", "grad.hip",
-           "expert_api.hip"]
+           "expert_api.hip", "norm.hip", "route.hip", "gate.hip",
+           "router_api.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -14,6 +14,20 @@ constexpr int kBlock = 256;               // 4 waves per workgroup
 constexpr int kWavesPerBlock = kBlock / kWave;
 constexpr int kTile = kBlock;             // tokens per scan tile (one per thread)
 
+// ---- launch sizes -----------------------------------------------------------
+// A launch may span at most 2^32-1 work-items per grid dimension, so the
+// largest grid in workgroups depends on the workgroup size.
+constexpr int64_t max_blocks(int threads) { return int64_t(UINT32_MAX) / threads; }
+
+// One workgroup of `threads` per item; grids beyond the work-item limit go
+// out as several launches, each told its first item.
+template <typename Launch>
+void for_each_launch(int64_t items, int threads, Launch launch) {
+  const int64_t most = max_blocks(threads);
+  for (int64_t i0 = 0; i0 < items; i0 += most)
+    launch(i0, unsigned(items - i0 < most ? items - i0 : most));
+}
+
 __device__ __forceinline__ int lane_id() { return threadIdx.x & (kWave - 1); }
 
 // Wave index as a value the compiler knows is uniform across the wave.
@@ -107,6 +121,20 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{lo, hi}, bf16x2_t));
 }
 
+// Eight bf16 values of a 16-byte piece as fp32, and back.
+__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(v[i]);
+    f[2 * i + 1] = bf16_hi(v[i]);
+  }
+}
+
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+  return u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+               pack_bf16x2(f[6], f[7])};
+}
+
 // ---- OCP e4m3 (float8_e4m3fn) encode ----------------------------------------
 // Nearest code with ties to even, saturating at 448 (0x7E; infinities too),
 // sign kept.  e4m3_encode_finite takes a non-NaN value; e4m3_encode also
@@ -132,6 +160,21 @@ __device__ __forceinline__ uint32_t e4m3_encode_finite(float v) {
 }
 __device__ __forceinline__ uint32_t e4m3_encode(float v) {
   return (__float_as_uint(v) & 0x7FFFFFFFu) > 0x7F800000u ? 0x7Fu : e4m3_encode_finite(v);
+}
+
+// Smallest power of two at or above s (s >= 0 and finite); 0 stays 0.  On
+// the bits: a normal value with a non-zero mantissa moves to the next
+// exponent; a subnormal mantissa m that is not a power of two becomes the
+// next power of two above m (2^23 being the smallest normal).
+__device__ __forceinline__ float pow2_ceil(float s) {
+  uint32_t u = __float_as_uint(s);
+  const uint32_t m = u & 0x7FFFFFu;
+  if (u >= 0x00800000u) {
+    if (m != 0u) u = (u & 0x7F800000u) + 0x00800000u;
+  } else if ((m & (m - 1u)) != 0u) {
+    u = 1u << (32 - __clz(m));
+  }
+  return __uint_as_float(u);
 }
 
 // ---- packed scan status words ------------------------------------------------

@@ -199,6 +199,21 @@ struct RowArgs {
 hipError_t launch_permute_bf16(const RowArgs& a, hipStream_t s);
 hipError_t launch_permute_fp8(const RowArgs& a, hipStream_t s);
 
+// Rows in 8 bits: H code bytes and `words` 32-bit scale words each.
+struct QuantRowArgs {
+  const void* q;
+  const void* scale;
+  int words;
+  int64_t T;
+  int H;
+  const int32_t* token_row;
+  int K;
+  int64_t capacity;
+  void* out;
+  void* out_scale;
+};
+hipError_t launch_permute_quantized(const QuantRowArgs& a, hipStream_t s);
+
 struct PadArgs {
   const int32_t* tokens_per_expert;  // [E_local] counts from the batched scan
   int E_local;

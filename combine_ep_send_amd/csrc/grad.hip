@@ -10,30 +10,6 @@ namespace {
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int64_t max_blocks(int threads) { return int64_t(UINT32_MAX) / threads; }
-
-// One workgroup of `threads` per item; grids beyond the limit of 2^32 - 1
-// work-items go out as several launches, each told its first item.
-template <typename Launch>
-void for_each_launch(int64_t items, int threads, Launch launch) {
-  const int64_t most = max_blocks(threads);
-  for (int64_t i0 = 0; i0 < items; i0 += most)
-    launch(i0, unsigned(items - i0 < most ? items - i0 : most));
-}
-
-__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_lo(v[i]);
-    f[2 * i + 1] = bf16_hi(v[i]);
-  }
-}
-
-__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
-  return u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-               pack_bf16x2(f[6], f[7])};
-}
-
 // 1 / (1 + exp(-g)): exp on the hardware's base-2 exponential, relative error
 // about |g| * 2^-23, and a reciprocal within one unit in the last place.  The
 // reciprocal instruction flushes results below 2^-126, so it takes a quarter of

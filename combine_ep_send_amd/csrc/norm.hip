@@ -1,0 +1,326 @@
+// RMS norm with the residual's addition and an 8-bit output, and its gradient
+// (gfx950, wave64).  A few operations a byte: HBM bounds both.
+#include "epdc_device.h"
+#include "router_launch.h"
+
+namespace epdc {
+
+namespace {
+
+constexpr int kNormMaxWaves = 16;
+constexpr int64_t kNormMaxGrid = 1 << 20;       // rows past it come round again
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// Sum over the workgroup, the same in every thread: lanes first, then waves in
+// order.  `part` alternates between two rows from one call to the next, so that
+// one barrier a call is enough.
+__device__ __forceinline__ float block_sum(float v, float* part) {
+  v = wave_sum(v);
+  const int waves = int(blockDim.x) / kWave;
+  if (waves == 1) return v;
+  if (lane_id() == 0) part[wave_id()] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int w = 0; w < waves; ++w) s += part[w];
+  return s;
+}
+
+// Eight weights of piece j.
+template <bool W32>
+__device__ __forceinline__ void load_weight(const void* weight, int j, float (&w)[8]) {
+  if constexpr (W32) {
+    const u32x4 lo = static_cast<const u32x4*>(weight)[2 * j];
+    const u32x4 hi = static_cast<const u32x4*>(weight)[2 * j + 1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = __uint_as_float(lo[i]);
+      w[4 + i] = __uint_as_float(hi[i]);
+    }
+  } else {
+    unpack8(static_cast<const u32x4*>(weight)[j], w);
+  }
+}
+
+// e4m3 codes and scale of 128 fp32 values held by 16 lanes, 8 each: the rules
+// of the dispatch's fp8 rows.  NaN is left out of amax; only a lane with one, or
+// a group with an infinity, needs the encoder that knows NaN.  A quotient passes
+// 448 by 2^-23 of it, or by more where the scale is subnormal; past 464 the
+// conversion instruction gives NaN, so the quotients are clamped first, which
+// is the saturation the codes call for.
+__device__ __forceinline__ u32x2 quantize_group(const float (&y)[8], bool pow2, float& scale) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+  const bool lane_nan = m > 0x7F800000u;
+  if (lane_nan) {
+    m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t u = __float_as_uint(y[i]) & 0x7FFFFFFFu;
+      if (u <= 0x7F800000u) m = max(m, u);
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
+  scale = __uint_as_float(m) / 448.0f;
+  if (pow2) scale = pow2_ceil(scale);
+  if (!lane_nan && m != 0x7F800000u) {
+    if (scale == 0.0f) return u32x2{0u, 0u};
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_fmed3f(y[i] / scale, -448.0f, 448.0f);
+    u32x2 c;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j], v[4 * j + 1], 0, false);
+      c[j] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j + 2], v[4 * j + 3], w, true));
+    }
+    return c;
+  }
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    c[i] = scale > 0.0f ? e4m3_encode(y[i] / scale) : (y[i] != y[i] ? 0x7Fu : 0u);
+  return u32x2{c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
+               c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24)};
+}
+
+// ---------------------------------------------------------------------------
+// Forward: one workgroup a row, the row in registers between the sum of squares
+// and the output, so that every byte moves once.  A thread's pieces lie a
+// workgroup apart: consecutive threads move consecutive 16-byte pieces, and 16
+// neighbours hold a 128-channel group.
+// ---------------------------------------------------------------------------
+template <int PT, bool W32>
+__global__ __launch_bounds__(kNormMaxWaves* kWave) void rms_norm_kernel(NormArgs a) {
+  __shared__ float part[2][kNormMaxWaves];
+  const int H8 = a.H >> 3, n = int(blockDim.x);
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    const u32x4* x = static_cast<const u32x4*>(a.x) + t * H8;
+    u32x4 v[PT], r[PT];
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int j = i * n + int(threadIdx.x);
+      v[i] = u32x4{0u, 0u, 0u, 0u};
+      if (j < H8) v[i] = x[j];
+    }
+    if (a.residual) {
+      const u32x4* res = static_cast<const u32x4*>(a.residual) + t * H8;
+#pragma unroll
+      for (int i = 0; i < PT; ++i) {
+        const int j = i * n + int(threadIdx.x);
+        r[i] = u32x4{0u, 0u, 0u, 0u};
+        if (j < H8) r[i] = res[j];
+      }
+      u32x4* ro = static_cast<u32x4*>(a.residual_out) + t * H8;
+#pragma unroll
+      for (int i = 0; i < PT; ++i) {
+        const int j = i * n + int(threadIdx.x);
+        float f[8], g[8];
+        unpack8(v[i], f);
+        unpack8(r[i], g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] += g[k];
+        v[i] = pack8(f);                    // the norm is of the row as it is kept
+        if (j < H8) ro[j] = v[i];
+      }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      float f[8];
+      unpack8(v[i], f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = __builtin_fmaf(f[k], f[k], sum);
+    }
+    const float rstd = 1.0f / sqrtf(block_sum(sum, part[turn]) / float(a.H) + a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int j = i * n + int(threadIdx.x);
+      if (j >= H8) continue;                // whole groups of 16 lanes where there are codes
+      float f[8], w[8];
+      unpack8(v[i], f);
+      load_weight<W32>(a.weight, j, w);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] = f[k] * rstd * w[k];
+      if (a.out) static_cast<u32x4*>(a.out)[t * H8 + j] = pack8(f);
+      if (a.q) {
+        float scale;
+        static_cast<u32x2*>(a.q)[t * H8 + j] = quantize_group(f, a.pow2, scale);
+        if ((j & 15) == 0) a.scale[t * (H8 >> 4) + (j >> 4)] = scale;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward: a workgroup takes rows in turn and keeps its sums of the weight's
+// gradient in registers; they go out as one row of partial sums a workgroup,
+// which a second launch adds up in order.
+// ---------------------------------------------------------------------------
+template <int PT, bool W32>
+__global__ __launch_bounds__(kNormMaxWaves* kWave) void rms_norm_backward_kernel(NormArgs a) {
+  __shared__ float part[2][kNormMaxWaves];
+  const int H8 = a.H >> 3, n = int(blockDim.x);
+  float w[PT][8], dw[PT][8];
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    const int j = i * n + int(threadIdx.x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[i][k] = dw[i][k] = 0.0f;
+    if (j < H8) load_weight<W32>(a.weight, j, w[i]);
+  }
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+    const u32x4* s = static_cast<const u32x4*>(a.x) + t * H8;
+    const u32x4* dy = static_cast<const u32x4*>(a.dy) + t * H8;
+    const u32x4* dr = static_cast<const u32x4*>(a.residual) + t * H8;
+    u32x4 sv[PT], dv[PT], rv[PT];
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int j = i * n + int(threadIdx.x);
+      sv[i] = dv[i] = rv[i] = u32x4{0u, 0u, 0u, 0u};
+      if (j < H8) {
+        sv[i] = s[j];
+        dv[i] = dy[j];
+        if (a.residual) rv[i] = dr[j];
+      }
+    }
+    const float rstd = a.rstd[t];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      float f[8], d[8];
+      unpack8(sv[i], f);
+      unpack8(dv[i], d);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float m = f[k] * rstd;
+        dw[i][k] = __builtin_fmaf(d[k], m, dw[i][k]);
+        sum = __builtin_fmaf(d[k] * w[i][k], m, sum);
+      }
+    }
+    const float mean = block_sum(sum, part[turn]) / float(a.H);
+    u32x4* dx = static_cast<u32x4*>(a.out) + t * H8;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int j = i * n + int(threadIdx.x);
+      if (j >= H8) continue;
+      float f[8], d[8], r[8];
+      unpack8(sv[i], f);
+      unpack8(dv[i], d);
+      unpack8(rv[i], r);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float v = rstd * (d[k] * w[i][k] - f[k] * rstd * mean);
+        d[k] = a.residual ? v + r[k] : v;
+      }
+      dx[j] = pack8(d);
+    }
+  }
+  if (!a.dweight) return;
+  u32x4* p = reinterpret_cast<u32x4*>(a.part) + int64_t(blockIdx.x) * (2 * H8);
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    const int j = i * n + int(threadIdx.x);
+    if (j >= H8) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      p[2 * j + h] = u32x4{__float_as_uint(dw[i][4 * h]), __float_as_uint(dw[i][4 * h + 1]),
+                           __float_as_uint(dw[i][4 * h + 2]), __float_as_uint(dw[i][4 * h + 3])};
+  }
+}
+
+// Sum of `rows` rows of partial sums: a workgroup takes 64 columns, 16 threads
+// of four columns each, 16 of them side by side over the rows.
+constexpr int kSumColumns = 64;
+__global__ __launch_bounds__(kBlock) void sum_rows_kernel(const float* part, int rows, int H,
+                                                          float* out) {
+  __shared__ float4 acc[16][16];
+  const int cx = int(threadIdx.x) & 15, ry = int(threadIdx.x) >> 4;
+  const int c = int(blockIdx.x) * kSumColumns + cx * 4;
+  float4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < H) {
+    for (int r = ry; r < rows; r += 16) {
+      const float4 v = *reinterpret_cast<const float4*>(part + int64_t(r) * H + c);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+  }
+  acc[ry][cx] = s;
+  __syncthreads();
+  if (ry != 0 || c >= H) return;
+#pragma unroll
+  for (int r = 1; r < 16; ++r) {
+    const float4 v = acc[r][cx];
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  // dweight may be 4-byte aligned only
+  out[c] = s.x;
+  out[c + 1] = s.y;
+  out[c + 2] = s.z;
+  out[c + 3] = s.w;
+}
+
+template <bool W32>
+void launch_norm_w(const NormArgs& a, hipStream_t s) {
+  const NormShape n = norm_shape(a.H);
+  const unsigned g = unsigned(a.T < kNormMaxGrid ? a.T : kNormMaxGrid);
+  if (n.pieces == 1)
+    rms_norm_kernel<1, W32><<<g, n.threads, 0, s>>>(a);
+  else if (n.pieces == 2)
+    rms_norm_kernel<2, W32><<<g, n.threads, 0, s>>>(a);
+  else if (n.pieces == 4)
+    rms_norm_kernel<4, W32><<<g, n.threads, 0, s>>>(a);
+  else
+    rms_norm_kernel<8, W32><<<g, n.threads, 0, s>>>(a);
+}
+
+template <bool W32>
+void launch_norm_backward_w(const NormArgs& a, unsigned g, hipStream_t s) {
+  const NormShape n = norm_shape(a.H);
+  if (n.pieces == 1)
+    rms_norm_backward_kernel<1, W32><<<g, n.threads, 0, s>>>(a);
+  else if (n.pieces == 2)
+    rms_norm_backward_kernel<2, W32><<<g, n.threads, 0, s>>>(a);
+  else if (n.pieces == 4)
+    rms_norm_backward_kernel<4, W32><<<g, n.threads, 0, s>>>(a);
+  else
+    rms_norm_backward_kernel<8, W32><<<g, n.threads, 0, s>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+  if (a.w32)
+    launch_norm_w<true>(a, s);
+  else
+    launch_norm_w<false>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s) {
+  const unsigned g = unsigned(norm_groups(a.T));
+  if (g > 0 && a.w32)
+    launch_norm_backward_w<true>(a, g, s);
+  else if (g > 0)
+    launch_norm_backward_w<false>(a, g, s);
+  if (a.dweight)                            // zeros for no rows
+    sum_rows_kernel<<<unsigned((a.H + kSumColumns - 1) / kSumColumns), kBlock, 0, s>>>(
+        a.part, int(g), a.H, a.dweight);
+  return hipGetLastError();
+}
+
+}  // namespace epdc

@@ -1,0 +1,444 @@
+// Choice of a token's experts from the router's logits, and the gradient of
+// its weights (gfx950, wave64).
+//
+// 16 or 64 lanes choose for a token.  Everything that decides is in 64 bits:
+// where scores lie so close that 32 bits would order them by their rounding,
+// the choice still is the formula's, and an fp64 operation takes no longer
+// here than an fp32 one.  A key's last ten bits give way to its expert's
+// number, so that one comparison orders by key, then by the lower number; a
+// key that is a logit has 29 spare bits and loses nothing.
+//
+// Each lane sorts what it holds and the lanes join their lists pairwise, the
+// largest K of both: the larger of a[i] and b[N-1-i] are the largest N, in an
+// order that log2(N) rounds of compare-exchange sort.
+#include "epdc_device.h"
+#include "router_launch.h"
+
+namespace epdc {
+
+namespace {
+
+// Below every key: those come from fp32 sums, and infinite ones are cut to
+// kLargest.
+constexpr double kNone = -1.7e308;
+constexpr double kLargest = 1.0e300;
+constexpr uint64_t kIndexBits = 1023;
+static_assert(kIndexBits >= 1024 - 1, "an expert's number fits");
+
+__device__ __forceinline__ double key_of(double v, int e) {
+  // +0.0 turns -0 into +0, which are equal
+  uint64_t b = __builtin_bit_cast(uint64_t, fmin(v, kLargest) + 0.0) & ~kIndexBits;
+  b |= (b >> 63) ? uint64_t(e) : kIndexBits - uint64_t(e);
+  return __builtin_bit_cast(double, b);
+}
+__device__ __forceinline__ int expert_of(double key) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, key);
+  const int c = int(b & kIndexBits);
+  return (b >> 63) ? c : int(kIndexBits) - c;
+}
+
+// The value of the partner lane at each step of a join over 2, 4, 8, 16, 32, 64
+// lanes: after a step all lanes of the block hold the same, so any pairing of
+// the two halves does.  Within 16 lanes by data-parallel moves.
+template <int STEP>
+__device__ __forceinline__ int partner(int v) {
+  if constexpr (STEP == 0) return __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xF, 0xF, false);
+  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xF, 0xF, false);
+  if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xF, 0xF, false);
+  if constexpr (STEP == 3) return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xF, 0xF, false);
+  return __shfl_xor(v, 1 << STEP);
+}
+template <int STEP>
+__device__ __forceinline__ double partner(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = uint32_t(partner<STEP>(int(uint32_t(b))));
+  const uint32_t hi = uint32_t(partner<STEP>(int(uint32_t(b >> 32))));
+  return __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
+}
+
+__device__ __forceinline__ double from_lane(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = uint32_t(__shfl(int(uint32_t(b)), lane));
+  const uint32_t hi = uint32_t(__shfl(int(uint32_t(b >> 32)), lane));
+  return __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
+}
+
+// Reduction over the LANES lanes of a token, the same in all of them.
+template <int LANES, int STEP = 0, typename Op>
+__device__ __forceinline__ double over_lanes(double v, Op op) {
+  if constexpr ((1 << STEP) < LANES)
+    return over_lanes<LANES, STEP + 1>(op(v, partner<STEP>(v)), op);
+  else
+    return v;
+}
+__device__ __forceinline__ double add(double a, double b) { return a + b; }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+
+__device__ __forceinline__ void exchange(double& a, double& b) {
+  const double hi = fmax(a, b);
+  b = fmin(a, b);
+  a = hi;
+}
+// A bitonic sequence into descending order.
+template <int N>
+__device__ __forceinline__ void merge(double (&v)[N]) {
+#pragma unroll
+  for (int j = N / 2; j > 0; j /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & j) == 0) exchange(v[i], v[i + j]);
+}
+template <int N>
+__device__ __forceinline__ void sort(double (&v)[N]) {
+#pragma unroll
+  for (int k = 2; k <= N; k *= 2)
+#pragma unroll
+    for (int j = k / 2; j > 0; j /= 2)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((i & j) == 0) {
+          if ((i & k) == 0)
+            exchange(v[i], v[i + j]);
+          else
+            exchange(v[i + j], v[i]);
+        }
+}
+
+// The lanes' descending lists of N into one of the largest KP.
+template <int LANES, int KP, int N, int STEP = 0>
+__device__ __forceinline__ void join(const double (&v)[N], double (&out)[KP]) {
+  if constexpr ((1 << STEP) >= LANES) {
+#pragma unroll
+    for (int i = 0; i < KP; ++i) out[i] = i < N ? v[i] : kNone;
+  } else if constexpr (N < KP) {
+    double w[2 * N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[i] = v[i];
+      w[2 * N - 1 - i] = partner<STEP>(v[i]);
+    }
+    merge(w);
+    join<LANES, KP, 2 * N, STEP + 1>(w, out);
+  } else {
+    double w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = fmax(v[i], partner<STEP>(v[N - 1 - i]));
+    merge(w);
+    join<LANES, KP, N, STEP + 1>(w, out);
+  }
+}
+
+// The largest KP (or all PER) of a lane's keys, descending.
+template <int KP, int PER>
+struct Local {
+  static constexpr int N = PER < KP ? PER : KP;
+  double v[N];
+  __device__ __forceinline__ explicit Local(const double (&k)[PER]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = k[i];
+    sort(v);
+#pragma unroll
+    for (int b = N; b < PER; b += N) {
+      double w[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = k[b + i];
+      sort(w);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = fmax(v[i], w[N - 1 - i]);
+      merge(v);
+    }
+  }
+};
+
+// exp(-|l|) and from it the sigmoid, without cancellation on either side.
+__device__ __forceinline__ double sigmoid(double l) {
+  const double x = exp(-fabs(l));
+  return (l >= 0.0 ? 1.0 : x) / (1.0 + x);
+}
+__device__ __forceinline__ double sigmoid_slope(double l) {
+  const double x = exp(-fabs(l));
+  return x / ((1.0 + x) * (1.0 + x));
+}
+
+// ---------------------------------------------------------------------------
+// Lane r of a group's `width` lanes holds the group's experts r, r + width, ...
+// (one group: all lanes).
+// ---------------------------------------------------------------------------
+template <int LANES, int PER, int KP>
+__global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width,
+                                                         int64_t block0) {
+  constexpr int kTokens = kBlock / LANES;
+  const int li = int(threadIdx.x) & (LANES - 1);
+  const int64_t t = (block0 + blockIdx.x) * kTokens + int(threadIdx.x) / LANES;
+  // every lane takes part in the moves; only the loads and stores are masked
+  const bool live = t < a.T && (!a.token_count || t < a.token_count[0]);
+  const int size = a.E / a.groups;
+  const int g = li / width, first = li & (width - 1);
+  const float* row = a.logits + t * a.E;
+  float l[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = j * width + first;
+    l[j] = -INFINITY;
+    if (live && g < a.groups && i < size) l[j] = row[g * size + i];
+  }
+  const bool by_score = a.bias || (a.groups > 1 && a.group_top == 2);
+  const bool whole = !a.sigmoid && (by_score || !a.renorm);
+  double most = 0.0, total = 1.0;
+  if (whole) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) m = fmaxf(m, l[j]);
+    most = over_lanes<LANES>(double(m), larger);
+    total = 0.0;
+  }
+  double k[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) k[j] = double(l[j]);
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const double p = exp(k[j] - most);
+      total += g < a.groups && j * width + first < size ? p : 0.0;
+      if (by_score) k[j] = p;
+    }
+    total = over_lanes<LANES>(total, add);
+    if (by_score) {
+      const double each = 1.0 / total;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) k[j] *= each;
+    }
+  } else if (by_score) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) k[j] = sigmoid(k[j]);
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = j * width + first;
+      if (g < a.groups && i < size) k[j] += double(a.bias[g * size + i]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    // false for a NaN on either side
+    if (!(l[j] > -INFINITY && k[j] > -INFINITY)) k[j] = kNone;
+  if (a.groups > 1) {
+    double b0 = kNone, b1 = kNone;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      b1 = fmax(b1, fmin(b0, k[j]));
+      b0 = fmax(b0, k[j]);
+    }
+    for (int o = 1; o < width; o <<= 1) {
+      const double c0 = __shfl_xor(b0, o), c1 = __shfl_xor(b1, o);
+      b1 = fmax(fmin(b0, c0), fmax(b1, c1));
+      b0 = fmax(b0, c0);
+    }
+    double worth = b0;
+    if (a.group_top == 2 && b1 > kNone) worth = b0 + b1;
+    if (b0 > kNone) worth = key_of(worth, g);
+    int before = 0;
+    for (int h = 0; h < a.groups; ++h)
+      before += from_lane(worth, (lane_id() & ~(LANES - 1)) + h * width) > worth ? 1 : 0;
+    if (before >= a.kept) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) k[j] = kNone;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (k[j] > kNone) k[j] = key_of(k[j], g * size + j * width + first);
+  double top[KP];
+  {
+    const Local<KP, PER> mine(k);
+    join<LANES, KP>(mine.v, top);
+  }
+  // lane i writes slot i
+  double mine = kNone;
+#pragma unroll
+  for (int i = 0; i < KP; ++i)
+    if (li == i) mine = top[i];
+  const bool chosen = li < a.K && mine > kNone;
+  const int e = chosen ? expert_of(mine) : -1;
+  double s = 0.0;
+  if (a.sigmoid) {
+    if (chosen) s = sigmoid(double(row[e]));
+  } else {
+    const float le = chosen ? row[e] : -INFINITY;
+    if (a.renorm) most = over_lanes<16>(double(le), larger);
+    if (chosen) s = exp(double(le) - most);
+  }
+  if (a.renorm) total = over_lanes<16>(s, add);
+  if (t >= a.T || li >= a.K) return;
+  a.topk_idx[t * a.K + li] = e;
+  // no sum: no weights
+  a.topk_weights[t * a.K + li] =
+      chosen && total != 0.0 ? float(double(a.scale) * s / total) : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// Gradient.  Lane k has slot k's share of the gradient, which goes to its
+// expert's place in a row in LDS; the lanes then write the row out, with what
+// a softmax's denominator adds for every expert.
+// ---------------------------------------------------------------------------
+template <int LANES, int PER>
+__global__ __launch_bounds__(kBlock) void route_backward_kernel(RouteArgs a, int64_t block0) {
+  constexpr int kTokens = kBlock / LANES;
+  __shared__ double grad[kTokens][LANES * PER];
+  const int li = int(threadIdx.x) & (LANES - 1);
+  const int64_t t = (block0 + blockIdx.x) * kTokens + int(threadIdx.x) / LANES;
+  const bool live = t < a.T;
+  double* g = grad[int(threadIdx.x) / LANES];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) g[j * LANES + li] = 0.0;
+  const float* row = a.logits + t * a.E;
+  int e = -1;
+  double d = 0.0;
+  if (live && li < a.K) {
+    const int64_t id = a.topk_idx[t * a.K + li];
+    if (id >= 0 && id < a.E) {
+      e = int(id);
+      d = double(a.scale) * double(a.dweights[t * a.K + li]);
+    }
+  }
+  const float le = e >= 0 ? row[e] : -INFINITY;
+  const bool any = over_lanes<LANES>(e >= 0 ? 1.0 : 0.0, add) > 0.0;
+  const bool whole = !a.sigmoid && !a.renorm;
+  double p[PER];                       // whole: exp(l - most) of the lane's experts
+  double most = 0.0, total = 1.0, s = 0.0, mean = 0.0;
+  if (whole) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = j * LANES + li;
+      const float l = live && i < a.E ? row[i] : -INFINITY;
+      p[j] = double(l);
+      m = fmaxf(m, l);
+    }
+    most = over_lanes<LANES>(double(m), larger);
+    total = 0.0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      p[j] = exp(p[j] - most);
+      if (j * LANES + li < a.E) total += p[j];
+    }
+    total = over_lanes<LANES>(total, add);
+  } else if (!a.sigmoid) {
+    most = over_lanes<16>(double(le), larger);
+  }
+  if (e >= 0)
+    s = a.sigmoid ? sigmoid(double(le)) : le == -INFINITY ? 0.0 : exp(double(le) - most);
+  if (a.renorm) total = over_lanes<16>(s, add);
+  const double each = total != 0.0 ? 1.0 / total : 0.0;
+  if (a.renorm || whole) {
+    // s / total: the weight among the chosen (renorm), or among all
+    mean = over_lanes<LANES>(d * (s * each), add);     // every lane needs it
+    if (a.sigmoid)
+      d = (d - mean) * each;
+    else
+      d = (whole ? d : d - mean) * (s * each);
+  }
+  if (a.sigmoid && e >= 0) d *= sigmoid_slope(double(le));
+  // an expert that several slots name: its first slot adds them up
+  bool first = e >= 0;
+  double sum = 0.0;
+  for (int k = 0; k < a.K; ++k) {
+    const int lane = (lane_id() & ~(LANES - 1)) + k;
+    const int ek = __shfl(e, lane);
+    const double dk = from_lane(d, lane);
+    if (ek == e) {
+      if (k < li) first = false;
+      sum += dk;
+    }
+  }
+  __syncthreads();                     // after the zeros
+  if (first) g[e] = sum;
+  __syncthreads();
+  if (!live) return;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = j * LANES + li;
+    if (i >= a.E) continue;
+    double v = g[i];
+    if (whole && any) v -= p[j] * each * mean;
+    a.dlogits[t * a.E + i] = float(v);
+  }
+}
+
+template <int LANES, int PER, int KP>
+void launch_route_k(const RouteArgs& a, hipStream_t s) {
+  const int64_t blocks = (a.T + kBlock / LANES - 1) / (kBlock / LANES);
+  const int width = LANES / ceil_pow2(a.groups);
+  for_each_launch(blocks, kBlock, [&](int64_t b0, unsigned g) {
+    route_kernel<LANES, PER, KP><<<g, kBlock, 0, s>>>(a, width, b0);
+  });
+}
+
+template <int LANES, int PER>
+void launch_route_per(const RouteArgs& a, hipStream_t s) {
+  if (a.K <= 2)
+    launch_route_k<LANES, PER, 2>(a, s);
+  else if (a.K <= 4)
+    launch_route_k<LANES, PER, 4>(a, s);
+  else if (a.K <= 8)
+    launch_route_k<LANES, PER, 8>(a, s);
+  else
+    launch_route_k<LANES, PER, 16>(a, s);
+}
+
+template <int LANES, int PER>
+void launch_route_backward_per(const RouteArgs& a, hipStream_t s) {
+  const int64_t blocks = (a.T + kBlock / LANES - 1) / (kBlock / LANES);
+  for_each_launch(blocks, kBlock, [&](int64_t b0, unsigned g) {
+    route_backward_kernel<LANES, PER><<<g, kBlock, 0, s>>>(a, b0);
+  });
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+  const RouteShape r = route_shape(a.E, a.groups);
+  if (r.lanes == 16) {
+    if (r.per == 1)
+      launch_route_per<16, 1>(a, s);
+    else if (r.per == 2)
+      launch_route_per<16, 2>(a, s);
+    else if (r.per == 4)
+      launch_route_per<16, 4>(a, s);
+    else if (r.per == 8)
+      launch_route_per<16, 8>(a, s);
+    else
+      launch_route_per<16, 16>(a, s);
+  } else if (r.per <= 8) {
+    launch_route_per<64, 8>(a, s);
+  } else if (r.per == 16) {
+    launch_route_per<64, 16>(a, s);
+  } else {
+    launch_route_per<64, 32>(a, s);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_route_backward(const RouteArgs& a, hipStream_t s) {
+  const RouteShape r = route_shape(a.E, 1);
+  if (r.lanes == 16) {
+    if (r.per == 1)
+      launch_route_backward_per<16, 1>(a, s);
+    else if (r.per == 2)
+      launch_route_backward_per<16, 2>(a, s);
+    else if (r.per == 4)
+      launch_route_backward_per<16, 4>(a, s);
+    else if (r.per == 8)
+      launch_route_backward_per<16, 8>(a, s);
+    else
+      launch_route_backward_per<16, 16>(a, s);
+  } else if (r.per <= 8) {
+    launch_route_backward_per<64, 8>(a, s);
+  } else {
+    launch_route_backward_per<64, 16>(a, s);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace epdc

@@ -131,21 +131,6 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
   return a | (b << 8) | (c << 16) | (d << 24);
 }
 
-// Smallest power of two at or above s (s >= 0 and finite); 0 stays 0.  On
-// the bits: a normal value with a non-zero mantissa moves to the next
-// exponent; a subnormal mantissa m that is not a power of two becomes the
-// next power of two above m (2^23 being the smallest normal).
-__device__ __forceinline__ float pow2_ceil(float s) {
-  uint32_t u = __float_as_uint(s);
-  const uint32_t m = u & 0x7FFFFFu;
-  if (u >= 0x00800000u) {
-    if (m != 0u) u = (u & 0x7F800000u) + 0x00800000u;
-  } else if ((m & (m - 1u)) != 0u) {
-    u = 1u << (32 - __clz(m));
-  }
-  return __uint_as_float(u);
-}
-
 template <int KMAX, int IT, int SFMT, bool LOAD_FIRST>
 __global__ __launch_bounds__(kWave) void permute_fp8_kernel(RowArgs a, int nchunks,
                                                             int64_t item0) {
@@ -290,6 +275,49 @@ __global__ __launch_bounds__(kWave) void permute_fp8_kernel(RowArgs a, int nchun
         st_stream(drow + p, q[it]);
         if ((p & ((1 << shift) - 1)) == 0) sbase[s0 + int64_t(p >> shift) * ustride] = sw[it];
       }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Permute of rows that are in 8 bits already: as the bf16 permute, a row being
+// H/16 pieces of codes and, after them, its scale words, one unit of SW words a
+// thread (a 16-byte piece where four divide a row's words and both arrays are
+// aligned, else a word).
+// ---------------------------------------------------------------------------
+template <int KMAX, bool WIDE>
+__global__ __launch_bounds__(kPermuteBlock) void permute_quantized_kernel(QuantRowArgs a,
+                                                                          int nchunks,
+                                                                          int64_t item0) {
+  const int codes = a.H >> 4;
+  const int units = WIDE ? a.words >> 2 : a.words;
+  const int64_t item = item0 + blockIdx.x;
+  const int64_t t = udiv(item, nchunks);
+  const int j = int(item - t * nchunks) * kPermuteBlock + int(threadIdx.x);
+  // loaded before the rows are known, as in the bf16 permute
+  u32x4 v{0u, 0u, 0u, 0u};
+  if (j < codes) {
+    v = static_cast<const u32x4*>(a.q)[t * codes + j];
+  } else if (j - codes < units) {
+    if (WIDE)
+      v = static_cast<const u32x4*>(a.scale)[t * units + (j - codes)];
+    else
+      v.x = static_cast<const uint32_t*>(a.scale)[t * units + (j - codes)];
+  }
+  int32_t rows[KMAX];
+  bool use[KMAX];
+  token_rows<KMAX>(a.token_row, t, a.K, a.capacity, rows, use);
+#pragma unroll
+  for (int k = 0; k < KMAX; ++k) {
+    if (!use[k]) continue;
+    if (j < codes) {
+      st_stream(static_cast<u32x4*>(a.out) + int64_t(rows[k]) * codes + j, v);
+    } else if (j - codes < units) {
+      const int64_t at = int64_t(rows[k]) * units + (j - codes);
+      if (WIDE)
+        static_cast<u32x4*>(a.out_scale)[at] = v;
+      else
+        static_cast<uint32_t*>(a.out_scale)[at] = v.x;
     }
   }
 }
@@ -536,10 +564,6 @@ __global__ __launch_bounds__(kSparseMaxBlock) void combine_sparse_kernel(Combine
 
 // ---- launch shapes -----------------------------------------------------------
 
-// A launch may span at most 2^32-1 work-items per grid dimension, so the
-// largest grid in workgroups depends on the workgroup size.
-constexpr int64_t max_blocks(int threads) { return int64_t(UINT32_MAX) / threads; }
-
 // Occupancy caps of the dense (token-major) permutes.  An unused dynamic LDS
 // allocation limits how many workgroups share a compute unit (160 KiB of LDS
 // each on gfx950): 18 KiB per 128-thread bf16 workgroup leaves room for 8 of
@@ -555,15 +579,6 @@ constexpr int64_t max_blocks(int threads) { return int64_t(UINT32_MAX) / threads
 constexpr unsigned kPermuteLdsCap = 18 * 1024;
 constexpr unsigned kFp8PermuteLdsCap = 10 * 1024;
 
-// One workgroup of `threads` per item; grids beyond the work-item limit go
-// out as several launches, each told its first item.
-template <typename Launch>
-void for_each_launch(int64_t items, int threads, Launch launch) {
-  const int64_t most = max_blocks(threads);
-  for (int64_t i0 = 0; i0 < items; i0 += most)
-    launch(i0, unsigned(items - i0 < most ? items - i0 : most));
-}
-
 // Split a row of `pieces` per-lane-sized units into the fewest chunks of at
 // most `most` units per lane, as evenly as possible.
 struct Split {
@@ -574,6 +589,21 @@ inline Split split_row(int64_t units, int most) {
   const int64_t per_lane = (units + kWave - 1) / kWave;
   const int64_t n = (per_lane + most - 1) / most;
   return Split{int(n), int((per_lane + n - 1) / n)};
+}
+
+template <int KMAX>
+void launch_permute_quantized_k(const QuantRowArgs& a, hipStream_t s) {
+  const bool wide = a.words % 4 == 0 && (reinterpret_cast<uintptr_t>(a.scale) & 15) == 0 &&
+                    (reinterpret_cast<uintptr_t>(a.out_scale) & 15) == 0;
+  const int units = (a.H >> 4) + (wide ? a.words >> 2 : a.words);
+  const int nchunks = (units + kPermuteBlock - 1) / kPermuteBlock;
+  for_each_launch(a.T * nchunks, kPermuteBlock, [&](int64_t i0, unsigned g) {
+    if (wide)
+      permute_quantized_kernel<KMAX, true><<<g, kPermuteBlock, kPermuteLdsCap, s>>>(a, nchunks, i0);
+    else
+      permute_quantized_kernel<KMAX, false><<<g, kPermuteBlock, kPermuteLdsCap, s>>>(a, nchunks,
+                                                                                    i0);
+  });
 }
 
 template <int KMAX>
@@ -696,6 +726,21 @@ hipError_t launch_permute_fp8(const RowArgs& a, hipStream_t s) {
     launch_permute_fp8_k<8>(a, s);
   else
     launch_permute_fp8_k<16>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_permute_quantized(const QuantRowArgs& a, hipStream_t s) {
+  if (a.T == 0) return hipSuccess;
+  if (a.K <= 2)
+    launch_permute_quantized_k<2>(a, s);
+  else if (a.K <= 4)
+    launch_permute_quantized_k<4>(a, s);
+  else if (a.K == 6)
+    launch_permute_quantized_k<6>(a, s);
+  else if (a.K <= 8)
+    launch_permute_quantized_k<8>(a, s);
+  else
+    launch_permute_quantized_k<16>(a, s);
   return hipGetLastError();
 }
 

@@ -18,6 +18,7 @@ from .ops import (Counts, Regrouped, SendLayout, ep_batched_prepare, ep_batched_
                   ep_counts_workspace_bytes, ep_dispatch_layout, ep_dispatch_layout_chunked,
                   ep_dispatch_layout_chunked_workspace_bytes, ep_dispatch_permute,
                   ep_layout_workspace_bytes, ep_regroup_by_expert, workspace_for)
+from .router import ep_dispatch_permute_quantized
 
 __all__ = [
     "chunk_bounds",
@@ -95,15 +96,18 @@ class DispatchHandle(NamedTuple):
     num_send: int
 
 
-def dispatch(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, *,
+def dispatch(x, topk_idx: torch.Tensor, topk_weights: torch.Tensor, *,
              num_local_experts: int, num_ranks: int, fp8: bool = False,
              num_send: Optional[int] = None):
     """Send each token once to every destination owning one of its experts
     (axolotl dispatch, group=None).  Returns (recv_x, recv_idx, recv_w,
     handle); recv_x is bf16 [N,H], or (e4m3 [N,H], fp32 scales [N,H/128])
-    with ``fp8``.  Without ``num_send`` the counts are copied to the host
-    once to size the buffers exactly; with it (a capacity, e.g. the worst
-    case T*min(K, P)) counts and layout run as one launch."""
+    with ``fp8``.  ``x`` is bf16 [T,H], or rows that are in 8 bits already, a
+    pair (e4m3 [T,H], fp32 scales [T,H/128]) as ep_rms_norm makes it (NeMo
+    uccl_ep Buffer.dispatch takes the same tuple): they are moved as they are
+    and ``fp8`` makes no difference.  Without ``num_send`` the counts are
+    copied to the host once to size the buffers exactly; with it (a capacity,
+    e.g. the worst case T*min(K, P)) counts and layout run as one launch."""
     T, K = topk_idx.shape
     if num_send is None:
         # exact sizing: counts, one host copy, then the layout
@@ -116,7 +120,11 @@ def dispatch(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor
         # given capacity: counts and layout in one launch, no host sync
         c, lay = ep_dispatch_layout(topk_idx, topk_weights, num_ranks, num_local_experts,
                                     num_send, expert_counts=False)
-    recv_x = ep_dispatch_permute(x, lay.token_row, num_send, fp8=fp8)
+    if isinstance(x, (tuple, list)):
+        q, scale = x
+        recv_x = ep_dispatch_permute_quantized(q, scale, lay.token_row, num_send)
+    else:
+        recv_x = ep_dispatch_permute(x, lay.token_row, num_send, fp8=fp8)
     handle = DispatchHandle(T, lay.token_row, topk_weights, lay.send_token_idx, lay.send_rank,
                             c.send_counts[0], int(num_send))
     return recv_x, lay.send_idx, lay.send_w, handle
@@ -239,10 +247,19 @@ class ChunkedDispatcher:
         """Index of chunk i's stream among ``nstreams`` (0 = the caller's)."""
         return i % nstreams
 
-    def forward(self, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+    def forward(self, x, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
                 local_kernel: Callable, *, out: Optional[torch.Tensor] = None, timer=None,
                 serialize: bool = False) -> torch.Tensor:
+        """``x``: bf16 [T, H], or with ``fp8`` also rows that are in 8 bits
+        already, a pair (e4m3 [T, H], fp32 scales [T, H/128])."""
         T, K, P, El, H = self.T, self.K, self.P, self.El, self.H
+        x_scale = None
+        if isinstance(x, (tuple, list)):
+            if not self.fp8:
+                raise ValueError("rows in 8 bits need a dispatcher with fp8")
+            x, x_scale = x
+            if tuple(x_scale.shape) != (T, H // 128):
+                raise ValueError(f"scales must be [{T}, {H // 128}]")
         if tuple(x.shape) != (T, H) or tuple(topk_idx.shape) != (T, K) or \
                 tuple(topk_weights.shape) != (T, K):
             raise ValueError(f"inputs must be x [{T}, {H}], topk_idx / topk_weights [{T}, {K}]")
@@ -319,7 +336,11 @@ class ChunkedDispatcher:
                     side_started.add(st)
             lay = self.layouts[i]
             tk = mark("permute_fp8" if self.fp8 else "permute", st)
-            if self.fp8:
+            if x_scale is not None:
+                recv_x = ep_dispatch_permute_quantized(x[a:b], x_scale[a:b], lay.token_row,
+                                                       self.caps[i], out=self.recv[i][0],
+                                                       out_scale=self.recv[i][1], stream=st)
+            elif self.fp8:
                 q, sc = self.recv[i]
                 ep_dispatch_permute(x[a:b], lay.token_row, self.caps[i], fp8=True, out=q,
                                     out_scale=sc, stream=st)
@@ -352,7 +373,7 @@ class ChunkedDispatcher:
         return out
 
 
-def dispatch_chunked_forward(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
+def dispatch_chunked_forward(x, topk_idx: torch.Tensor, topk_weights: torch.Tensor,
                              local_kernel: Callable, *, num_local_experts: int, num_ranks: int,
                              chunks: int, fp8: bool = False, streams=None,
                              exact_counts: bool = True) -> torch.Tensor:
@@ -360,15 +381,17 @@ def dispatch_chunked_forward(x: torch.Tensor, topk_idx: torch.Tensor, topk_weigh
     alternating over HIP streams (axolotl dispatch_chunked_forward): one
     ChunkedDispatcher forward.  ``local_kernel(recv_x, recv_idx, recv_w)``
     returns the bf16 expert output [rows, H] of one chunk (recv_x is
-    (e4m3 rows, scales) with ``fp8``); it runs on the chunk's stream.  With
+    (e4m3 rows, scales) with ``fp8``, where ``x`` too may be such a pair);
+    it runs on the chunk's stream.  With
     ``exact_counts`` (the default, as on the page) the split counts of every
     chunk reach the host in one copy; otherwise each chunk gets the worst
     case T_c * min(K, P) rows and nothing waits on the host."""
     T, K = topk_idx.shape
-    d = ChunkedDispatcher(T, K, x.shape[1], num_local_experts=num_local_experts,
+    rows = x[0] if isinstance(x, (tuple, list)) else x
+    d = ChunkedDispatcher(T, K, rows.shape[1], num_local_experts=num_local_experts,
                           num_ranks=num_ranks, chunks=chunks, fp8=fp8,
                           streams=streams if streams is not None else 2,
-                          exact_counts=exact_counts, device=x.device)
+                          exact_counts=exact_counts, device=rows.device)
     return d.forward(x, topk_idx, topk_weights,
                      lambda i, rx, ri, rw: local_kernel(rx, ri, rw))
 

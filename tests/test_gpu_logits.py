@@ -1,0 +1,118 @@
+"""The router's logits and their gradients against 64 bits."""
+
+import numpy as np
+import pytest
+import torch
+
+import combine_ep_send_amd as ep
+from tests.router_forms import bf16, check, f64, logits_backward_ref, logits_ref
+
+pytestmark = pytest.mark.gpu
+
+# one token and one expert; tiles that end inside; each number of rows and
+# experts a workgroup takes; channels split over workgroups or not; several
+# workgroups of experts
+SHAPES = [(1, 1, 8), (1, 256, 7168), (3, 8, 512), (16, 64, 256), (17, 60, 1000), (33, 130, 2056),
+          (65, 7, 4096), (130, 256, 264), (257, 64, 520), (20, 1024, 1032), (9, 300, 65536),
+          (4200, 128, 320), (4200, 250, 136), (4160, 64, 72), (9000, 96, 64)]
+
+
+def make(T, E, H, seed):
+    rng = np.random.default_rng(seed)
+    x = bf16(rng.standard_normal((T, H)))
+    w = bf16(rng.standard_normal((E, H)) / np.sqrt(H))
+    return rng, x, w
+
+
+@pytest.mark.parametrize("T,E,H", SHAPES)
+def test_logits(T, E, H):
+    _, x, w = make(T, E, H, T + E + H)
+    got = ep.ep_router_logits(x.cuda(), w.cuda())
+    check(got, *logits_ref(f64(x), f64(w)))
+
+
+@pytest.mark.parametrize("T,E,H", SHAPES)
+def test_backward(T, E, H):
+    rng, x, w = make(T, E, H, 2 * T + E + H)
+    dl = (rng.standard_normal((T, E)) * rng.uniform(0.01, 10, (T, 1))).astype(np.float32)
+    d = torch.from_numpy(dl).cuda()
+    dx, dw = ep.ep_router_logits_backward(d, x.cuda(), w.cuda())
+    rx, tx, rw, tw = logits_backward_ref(dl.astype(np.float64), f64(x), f64(w))
+    check(dx, rx, tx, "dx")
+    check(dw, rw, tw, "dw")
+    only, none = ep.ep_router_logits_backward(d, None, w.cuda(), weight_grad=False)
+    assert none is None and torch.equal(only, dx)
+    none, only = ep.ep_router_logits_backward(d, x.cuda(), None, input_grad=False)
+    assert none is None and torch.equal(only, dw)
+
+
+def test_small_numbers_are_exact():
+    """Whole numbers whose sums fit fp32: every product and sum is exact, whatever
+    the order, and the parts of the logits' gradient are too (17 bits and up)."""
+    rng = np.random.default_rng(2)
+    T, E, H = 100, 72, 648
+    x, w = rng.integers(-8, 9, (T, H)), rng.integers(-8, 9, (E, H))
+    got = ep.ep_router_logits(bf16(x * 1.0).cuda(), bf16(w * 1.0).cuda())
+    assert np.array_equal(f64(got), x @ w.T)
+    dl = rng.integers(-(1 << 20), 1 << 20, (T, E))
+    one = np.sign(rng.integers(-3, 4, (T, H)))
+    one[rng.random((T, H)) < 0.9] = 0                # few terms: sums below 2^24
+    _, dw = ep.ep_router_logits_backward(torch.from_numpy(dl).float().cuda(),
+                                         bf16(one * 1.0).cuda(), None, input_grad=False)
+    keep = np.abs(dl).T @ np.abs(one) < 1 << 24
+    assert keep.mean() > 0.5
+    assert np.array_equal(f64(dw)[keep], (dl.T @ one)[keep])
+
+
+def test_infinities_and_nan_stay_in_their_rows():
+    _, x, w = make(40, 20, 256, 6)
+    x[3, 7], x[5, 0] = float("nan"), float("inf")
+    w[11, 9] = float("nan")
+    got = ep.ep_router_logits(x.cuda(), w.cuda()).cpu()
+    assert got[3].isnan().all() and got[:, 11].isnan().all()
+    assert not got[5, :11].isfinite().any()
+    rest = np.delete(np.delete(f64(got), [3, 5], 0), 11, 1)
+    ref, tol = logits_ref(np.delete(f64(x), [3, 5], 0), np.delete(f64(w), 11, 0))
+    check(rest, ref, tol)
+    d = torch.randn(40, 20)
+    d[2, 4], d[9, 6] = float("inf"), float("nan")
+    d[12, 1] = 3.4e38                                # past the largest bf16
+    _, x, w = make(40, 20, 256, 7)
+    dx, dw = ep.ep_router_logits_backward(d.cuda(), x.cuda(), w.cuda())
+    bad = [2, 9, 12]
+    rx, tx, rw, tw = logits_backward_ref(f64(d), f64(x), f64(w))
+    check(np.delete(f64(dx), bad, 0), np.delete(rx, bad, 0), np.delete(tx, bad, 0))
+    check(np.delete(f64(dw), [4, 6, 1], 0), np.delete(rw, [4, 6, 1], 0),
+          np.delete(tw, [4, 6, 1], 0))
+    assert not dx.cpu()[bad].isfinite().any() and dw.cpu()[6].isnan().all()
+    # an infinity takes part as one, not as a NaN
+    assert torch.equal(dw.cpu()[4], torch.where(x[2].float() > 0, float("inf"), -float("inf")))
+
+
+def test_no_tokens_given_outputs_and_refusals():
+    _, x, w = make(10, 12, 128, 1)
+    x, w, d = x.cuda(), w.cuda(), torch.randn(10, 12).cuda()
+    out = torch.empty(10, 12).cuda()
+    assert ep.ep_router_logits(x, w, out=out) is out
+    assert torch.equal(out, ep.ep_router_logits(x, w))
+    assert ep.ep_router_logits(x[:0], w).shape == (0, 12)
+    dx, dw = ep.ep_router_logits_backward(d[:0], x[:0], w, dw=torch.ones(12, 128).cuda())
+    assert dx.shape == (0, 128) and (dw == 0).all()
+    ws = torch.empty(ep.ep_router_logits_backward_workspace_bytes(10, 12, 128),
+                     dtype=torch.uint8).cuda()
+    a = ep.ep_router_logits_backward(d, x, w)
+    b = ep.ep_router_logits_backward(d, x, w, workspace=ws, dx=torch.empty_like(x),
+                                     dw=torch.empty(12, 128).cuda())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for fn, match in ((lambda: ep.ep_router_logits(x, w[:, :64].contiguous()), "channels"),
+                      (lambda: ep.ep_router_logits(x, w.float()), "bfloat16"),
+                      (lambda: ep.ep_router_logits(x, w, workspace=ws[:16]), "workspace"),
+                      (lambda: ep.ep_router_logits(x[:, ::2], w), "contiguous"),
+                      (lambda: ep.ep_router_logits_backward(d, x, None), "needs w"),
+                      (lambda: ep.ep_router_logits_backward(d, None, w), "needs x"),
+                      (lambda: ep.ep_router_logits_backward(d, x, w, workspace=ws[256:]), "workspace"),
+                      (lambda: ep.ep_router_logits_backward(d, x, w, input_grad=False,
+                                                            weight_grad=False), "asked"),
+                      (lambda: ep.ep_router_logits_backward(d, x, w, input_grad=False, dx=x), "input_grad")):
+        with pytest.raises(ValueError, match=match):
+            fn()

@@ -1,0 +1,207 @@
+"""RMS norm with the residual's addition and the 8-bit output, and its gradient,
+against 64 bits."""
+
+import numpy as np
+import pytest
+import torch
+
+import combine_ep_send_amd as ep
+from tests.router_forms import (BF16, E4M3, F32, TINY, bf16, check, f64, norm_backward_ref,
+                                norm_ref)
+
+pytestmark = pytest.mark.gpu
+
+# one token; odd rows; one lane's piece; a wave; several pieces a thread; past the
+# workgroups of the backward; the most channels
+SHAPES = [(1, 8), (1, 7168), (3, 128), (77, 520), (5, 4104), (1500, 256), (2, 16384), (2, 65536)]
+
+
+def make(T, H, seed, f32, residual=True):
+    rng = np.random.default_rng(seed)
+    x = bf16(rng.standard_normal((T, H)) * rng.uniform(0.1, 4, (T, 1)))
+    r = bf16(rng.standard_normal((T, H))) if residual else None
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(H))
+    return rng, x, r, w.float() if f32 else w.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+@pytest.mark.parametrize("f32", [False, True])
+def test_forward(T, H, f32):
+    _, x, r, w = make(T, H, T + H, f32)
+    n = ep.ep_rms_norm(x.cuda(), w.cuda(), 1e-5, residual=r.cuda(), rstd=True)
+    s = (x.float() + r.float()).to(torch.bfloat16)
+    assert torch.equal(n.residual.cpu(), s)
+    rstd, rtol, y, tol = norm_ref(f64(s), f64(w), float(np.float32(1e-5)))
+    check(n.rstd, rstd, rtol, "rstd")
+    check(n.y, y, tol + BF16 * np.abs(y) + TINY, "y")
+    assert n.q is None and n.scale is None
+    plain = ep.ep_rms_norm(s.cuda(), w.cuda(), 1e-5)
+    assert torch.equal(plain.y, n.y) and plain.residual is None and plain.rstd is None
+
+
+@pytest.mark.parametrize("T,H", [(1, 128), (1, 7168), (77, 640), (3, 16384)])
+@pytest.mark.parametrize("fmt", ["f32", "pow2"])
+@pytest.mark.parametrize("f32", [False, True])
+def test_codes_and_scales(T, H, fmt, f32):
+    _, x, _, w = make(T, H, T * 3 + H, f32)
+    both = ep.ep_rms_norm(x.cuda(), w.cuda(), fp8=True, scale_fmt=fmt)
+    alone = ep.ep_rms_norm(x.cuda(), w.cuda(), fp8=True, bf16=False, scale_fmt=fmt)
+    assert alone.y is None
+    assert torch.equal(alone.q.view(torch.uint8), both.q.view(torch.uint8))
+    assert torch.equal(alone.scale, both.scale)
+    _, _, y, tol = norm_ref(f64(x), f64(w), float(np.float32(1e-6)))
+    check(both.y, y, tol + BF16 * np.abs(y) + TINY, "y")
+    amax = np.abs(y).reshape(T, -1, 128).max(-1) / 448
+    near = (tol / np.maximum(np.abs(y), 1e-30)).max() + 2 * F32
+    scale = f64(both.scale)
+    if fmt == "f32":
+        check(scale, amax, amax * near, "scale")
+    else:
+        assert (np.frexp(scale)[0] == 0.5).all()
+        assert (scale >= amax * (1 - near)).all() and (scale < 2 * amax * (1 + near)).all()
+    v = f64(both.q.float()).reshape(T, -1, 128) * scale[..., None]
+    step = E4M3 * np.abs(y).reshape(v.shape) + 2.0 ** -10 * scale[..., None]
+    check(v, y.reshape(v.shape), step * (1 + 1e-5) + tol.reshape(v.shape), "codes")
+
+
+def test_codes_are_those_of_the_dispatch():
+    """Rows that need no rounding on the way: signs times a power of two, rstd and
+    weight powers of two, so that bf16 holds y and both quantizers see the same."""
+    g = torch.Generator().manual_seed(1)
+    T, H = 9, 512
+    x = torch.where(torch.rand(T, H, generator=g) < 0.5, -1.0, 1.0)
+    w = torch.exp2(torch.randint(-9, 4, (H,), generator=g).float()) * 1.375
+    n = ep.ep_rms_norm(x.to(torch.bfloat16).cuda(), w.cuda(), 0.0, fp8=True)
+    row = torch.arange(T, dtype=torch.int32)[:, None].cuda()
+    q, scale = ep.ep_dispatch_permute(n.y, row, T, fp8=True)
+    assert torch.equal(q.view(torch.uint8), n.q.view(torch.uint8))
+    assert torch.equal(scale, n.scale)
+
+
+def test_rows_of_zeros_infinities_and_nan():
+    H = 256
+    x = torch.ones(5, H)
+    x[0] = 0.0
+    x[1, 3] = float("inf")
+    x[2, 130] = float("nan")
+    x[3, 128:] = 0.0
+    x[4] = 1e-38
+    w = torch.ones(H)
+    w[200] = 0.0
+    n = ep.ep_rms_norm(x.to(torch.bfloat16).cuda(), w.cuda(), 1e-6, fp8=True, rstd=True)
+    y, q, scale = n.y.float().cpu(), n.q.view(torch.uint8).cpu(), n.scale.cpu()
+    assert (y[0] == 0).all() and (q[0] == 0).all() and (scale[0] == 0).all()
+    # an infinite mean square: rstd 0, so NaN at the infinity and 0 elsewhere
+    assert n.rstd[1] == 0 and y[1, 3].isnan() and (y[1, :3] == 0).all()
+    assert q[1, 3] == 0x7F and (q[1, 128:] == 0).all() and (scale[1] == 0).all()
+    assert y[2].isnan().all() and (q[2] == 0x7F).all() and (scale[2] == 0).all()
+    assert scale[3, 0] > 0 and scale[3, 1] == 0 and (q[3, 128:] == 0).all()
+    # tiny rows beside eps: finite, scale at the bottom of fp32
+    assert torch.isfinite(y[4]).all() and ((q[4] & 0x7F) != 0x7F).all()
+    tiny = ep.ep_rms_norm(x[:1].to(torch.bfloat16).cuda() + 1, torch.full((H,), 1e-43).cuda(), 0.0,
+                          fp8=True)
+    # y is about 71 of fp32's least steps, amax / 448 rounds to none: zeros
+    assert (tiny.scale == 0).all() and (tiny.q.view(torch.uint8) == 0).all()
+    # 700 steps: a scale of 2 steps, quotients past 448 are cut to it
+    tiny = ep.ep_rms_norm(x[:1].to(torch.bfloat16).cuda() + 1,
+                          torch.full((H,), 700 * 2.0 ** -149).cuda(), 0.0, fp8=True)
+    assert (tiny.scale == 2 * 2.0 ** -149).all()
+    assert (tiny.q.float() == 352).all()            # 350 between 320 and 352
+
+
+def test_in_place_and_given_outputs():
+    _, x, r, w = make(33, 1024, 5, False)
+    x, r, w = x.cuda(), r.cuda(), w.cuda()
+    want = ep.ep_rms_norm(x, w, residual=r, fp8=True, rstd=True)
+    r2 = r.clone()
+    y = torch.empty_like(x)
+    got = ep.ep_rms_norm(x, w, residual=r2, fp8=True, rstd=True, residual_out=r2, out=y,
+                         q=torch.empty_like(want.q), scale=torch.empty_like(want.scale),
+                         rstd_out=torch.empty_like(want.rstd))
+    assert got.residual is r2 and got.y is y
+    x2 = x.clone()
+    over = ep.ep_rms_norm(x2, w, residual=r, residual_out=x2)
+    for a, b in ((got.residual, want.residual), (got.y, want.y), (got.scale, want.scale),
+                 (got.rstd, want.rstd), (got.q.view(torch.uint8), want.q.view(torch.uint8)),
+                 (over.residual, want.residual), (over.y, want.y)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,H", SHAPES + [(4099, 512)])
+@pytest.mark.parametrize("f32,residual", [(False, True), (True, False)])
+def test_backward(T, H, f32, residual):
+    rng, s, _, w = make(T, H, T + 2 * H, f32, False)
+    dy, dr = bf16(rng.standard_normal((T, H))), bf16(rng.standard_normal((T, H)))
+    rstd = 1 / np.sqrt((f64(s) ** 2).mean(1) + 1e-6)
+    rstd32 = torch.from_numpy(rstd).float()
+    dx, tol, dw, dtol = norm_backward_ref(f64(dy), f64(s), f64(w), f64(rstd32),
+                                          f64(dr) if residual else None)
+    got, gw = ep.ep_rms_norm_backward(dy.cuda(), s.cuda(), w.cuda(), rstd32.cuda(),
+                                      d_residual=dr.cuda() if residual else None)
+    check(got, dx, tol, "dx")
+    check(gw, dw, dtol, "dw")
+    alone, none = ep.ep_rms_norm_backward(dy.cuda(), s.cuda(), w.cuda(), rstd32.cuda(),
+                                          d_residual=dr.cuda() if residual else None,
+                                          weight_grad=False)
+    assert none is None and torch.equal(alone, got)
+
+
+def test_backward_in_place_and_no_tokens():
+    rng, s, _, w = make(50, 264, 8, False, False)
+    dy, dr = bf16(rng.standard_normal((50, 264))).cuda(), bf16(rng.standard_normal((50, 264))).cuda()
+    s, w = s.cuda(), w.cuda()
+    rstd = ep.ep_rms_norm(s, w, rstd=True).rstd
+    want, dw = ep.ep_rms_norm_backward(dy, s, w, rstd, d_residual=dr)
+    over = dr.clone()
+    got, dw2 = ep.ep_rms_norm_backward(dy, s, w, rstd, d_residual=over, out=over)
+    assert got is over and torch.equal(got, want) and torch.equal(dw, dw2)
+    over = dy.clone()
+    got, _ = ep.ep_rms_norm_backward(over, s, w, rstd, d_residual=dr, out=over)
+    assert torch.equal(got, want)
+    none, dw = ep.ep_rms_norm_backward(dy[:0], s[:0], w, rstd[:0], dw=torch.ones(264).cuda())
+    assert none.shape == (0, 264) and (dw == 0).all()
+    empty = ep.ep_rms_norm(s[:0], w, residual=s[:0])
+    assert empty.y.shape == empty.residual.shape == (0, 264)
+
+
+def test_gradient_against_differences():
+    """The gradient of sum(c * y) along a direction, from the forward itself in
+    64-bit sums.  The forward's bf16 output is off by 2^-8 of a value at each end;
+    what is left is of second order in the step."""
+    rng, x, r, w = make(4, 512, 21, True)
+    c, v = bf16(rng.standard_normal((4, 512))), rng.standard_normal((4, 512))
+    n = ep.ep_rms_norm(x.cuda(), w.cuda(), residual=r.cuda(), rstd=True)
+    dx, _ = ep.ep_rms_norm_backward(c.cuda(), n.residual, w.cuda(), n.rstd)
+    s, h = f64(n.residual), 1e-4
+
+    def value(a):
+        rstd = 1 / np.sqrt((a * a).mean(1) + 1e-6)
+        return (f64(c) * a * rstd[:, None] * f64(w)).sum()
+    slope = (value(s + h * v) - value(s - h * v)) / (2 * h)
+    got = (f64(dx) * v).sum()
+    # dx's rounding, element by element, and the differences' own
+    assert abs(got - slope) <= 1.1 * BF16 * np.abs(f64(dx) * v).sum() + 1e-5
+
+
+def test_refusals():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16).cuda()
+    w = torch.ones(256).cuda()
+    for kw, match in ((dict(bf16=False), "asked"), (dict(residual_out=x), "residual"),
+                      (dict(q=x), "fp8"), (dict(rstd_out=w), "rstd"), (dict(scale_fmt="ue8m0", fp8=True), "scale_fmt"),
+                      (dict(residual=x[:3]), "shape"), (dict(residual=x.float()), "bfloat16"),
+                      (dict(out=x.t()), "contiguous"), (dict(bf16=False, fp8=True, out=x), "bf16"),
+                      (dict(eps=-1.0), "argument"), (dict(eps=float("inf")), "argument")):
+        with pytest.raises(ValueError, match=match):
+            ep.ep_rms_norm(x, w, **kw)
+    with pytest.raises(ValueError, match="contiguous"):
+        ep.ep_rms_norm(x[:, ::2], w[:128])
+    with pytest.raises(ValueError, match="shape"):
+        ep.ep_rms_norm(x, w[:128])
+    with pytest.raises(ValueError, match="128"):
+        ep.ep_rms_norm(x[:, :8].contiguous(), w[:8], fp8=True)
+    with pytest.raises(ValueError):
+        ep.ep_rms_norm(x[:, :12].contiguous(), w[:12])
+    with pytest.raises(ValueError, match="workspace"):
+        ep.ep_rms_norm_backward(x, x, w, w[:4], workspace=torch.empty(8, dtype=torch.uint8).cuda())
+    with pytest.raises(ValueError, match="weight_grad"):
+        ep.ep_rms_norm_backward(x, x, w, w[:4], weight_grad=False, dw=w)
