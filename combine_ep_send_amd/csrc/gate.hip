@@ -2,7 +2,7 @@
 // which one side is small.  The matrix cores take bf16 and sum in fp32
 // (v_mfma_f32_16x16x32_bf16); what is fp32 (the logits' gradient) takes part as
 // the sum of two or three bf16 numbers.
-#include "epdc_device.h"
+#include "router_device.h"
 #include "router_launch.h"
 
 namespace epdc {
@@ -30,160 +30,172 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-struct GemmArgs {
-  const void* a;                 // [parts][M][lda] bf16
-  const void* b;                 // [N][ldb] bf16
-  int64_t M;
-  int N, K;
-  int lda, ldb;                  // elements, multiples of 8
-  int64_t plane;                 // elements from part to part of a
-  int each;                      // stages a workgroup takes
-  void* out;                     // [M][N] bf16, or fp32 [splits][M][N]
+// The order of a stage's instructions: its 2 M products with, between them, READS
+// LDS reads, the WRITES writes, READS further reads and WRITES loads.
+template <int M, int READS, int WRITES>
+__device__ __forceinline__ void interleave() {
+  constexpr int kProduct = 0x008, kLoad = 0x020, kRead = 0x100, kWrite = 0x200;
+#pragma unroll
+  for (int i = 0; i < READS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < M - READS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kWrite, (WRITES + M - READS - 1) / (M - READS), 0);
+  }
+#pragma unroll
+  for (int i = 0; i < READS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < M - READS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kLoad, (WRITES + M - READS - 1) / (M - READS), 0);
+  }
+}
+
+struct LogitsGemm {
+  const void* x;                 // [T][H] bf16
+  const void* w;                 // [E][H] bf16
+  int64_t T;
+  int E, H;
+  int each;                      // stages of 64 channels a workgroup takes
+  float* out;                    // [splits][T][E]
 };
 
 // ---------------------------------------------------------------------------
-// out[m, n] = sum over k of A[m, k] B[n, k], A the sum of PARTS bf16 arrays.
-// The rows of A go through LDS, which the waves side by side along n share; a
-// wave's rows of B come straight into its registers, in a ring of D stages with
-// the rows of A.  Loads go through descriptors whose range check gives zeros for
-// rows and channels past the end, so nothing branches.
-// LDS holds a row of a stage as 16-byte pieces, piece p at p ^ (row & 7): the
-// eight rows that a read takes at once then lie in different banks.
+// out[t, e] = sum over h of x[t, h] w[e, h].  A workgroup takes 16 MT WM tokens
+// and 64 WN experts, a wave 16 MT of the former and 64 of the latter; a stage is
+// 64 channels of both.  Eight lanes load 128 bytes of a row into a ring of R
+// stages in registers; from there a stage goes to one of three buffers in LDS,
+// two stages before it is used, so that behind the one barrier of a stage the
+// fragments of its first products are in registers already, and loads, LDS
+// writes and reads all run between the products.  (Fragments loaded straight
+// from memory have neighbouring lanes in different rows, and a load of 1 KB then
+// takes 70 cycles: 129 us for 16384 tokens, 256 experts, 7168 channels.)
+// Loads go through descriptors whose range check gives zeros for rows and
+// channels past the end.
+// LDS holds a row of a stage as eight 16-byte pieces, permuted by three bits of
+// the row, so that the eight rows that a read takes at once lie in different
+// banks.  w is the instruction's first operand, so that a lane's four results
+// are neighbouring experts, and row r of tile i is row (r / 4) * 16 + i * 4 + r % 4
+// of the wave's 64, so that its four tiles are too.
 // ---------------------------------------------------------------------------
-template <int MT, int WN, int PARTS, bool BF16OUT>
-__global__ __launch_bounds__(kBlock) void gemm_kernel(GemmArgs g, int64_t mb0) {
-  constexpr int WK = 4 / WN, BM = 16 * MT, D = 2;
-  constexpr int P = 8 * WK;                              // pieces of a row and stage
-  constexpr int LOADS = (BM * P + kBlock - 1) / kBlock;  // pieces of A a thread loads, a part
-  constexpr int kBuffers = 2 * PARTS * BM * P;
-  constexpr int kReduce = WK > 1 ? WK * BM * WN * 64 / 4 : 0;
-  __shared__ u32x4 lds[kBuffers > kReduce ? kBuffers : kReduce];
+template <int MT, int WM, int WN>
+__global__ __launch_bounds__(kBlock) void logits_kernel(LogitsGemm g, int64_t mb0) {
+  static_assert(WM * WN == 4, "four waves");
+  constexpr int BM = 16 * MT * WM, BN = 64 * WN, R = 3;
+  constexpr int kA = BM * 8, kB = BN * 8;                // pieces of a stage
+  constexpr int LA = (kA + kBlock - 1) / kBlock, LB = kB / kBlock;
+  __shared__ u32x4 lds[3 * (kA + kB)];
   const int lane = lane_id(), n = lane & 15, q = lane >> 4;
-  const int wn = wave_id() % WN, wk = wave_id() / WN;
+  const int wn = wave_id() % WN, wm = wave_id() / WN;
   const int64_t m0 = (mb0 + blockIdx.x) * BM;
-  const int n0 = int(blockIdx.y) * (64 * WN);
-  const int rows = int(g.M - m0 < BM ? g.M - m0 : BM);
-  const int cols = g.N - n0 < 64 * WN ? g.N - n0 : 64 * WN;
-  rsrc_t ar[PARTS];
+  const int n0 = int(blockIdx.y) * BN;
+  const int rows = int(g.T - m0 < BM ? g.T - m0 : BM);
+  const int cols = g.E - n0 < BN ? g.E - n0 : BN;
+  const int pitch = 2 * g.H;                             // bytes of a row
+  const rsrc_t ar = make_rsrc(static_cast<const uint16_t*>(g.x) + m0 * g.H, int64_t(rows) * pitch);
+  const rsrc_t br = make_rsrc(static_cast<const uint16_t*>(g.w) + int64_t(n0) * g.H,
+                              int64_t(cols) * pitch);
+  const int stages = (g.H + 63) / 64;
+  const int st0 = int(blockIdx.z) * g.each;
+  const int count = stages - st0 < g.each ? stages - st0 : g.each;
+  const int row0 = int(threadIdx.x) >> 3, piece = int(threadIdx.x) & 7;
+  const uint32_t off0 = uint32_t(row0) * uint32_t(pitch) + uint32_t(piece * 16);
+  const uint32_t step = 32u * uint32_t(pitch);
+  // rows: piece p of row r lies at p ^ a(r), p ^ b(r)
+  const int awrite = row0 * 8 + (piece ^ (row0 & 7));
+  const int bwrite = kA + row0 * 8 + (piece ^ ((row0 & 3) | ((row0 >> 2) & 4)));
+  u32x4 av[R][LA], bv[R][LB];
+  auto load = [&](int d, int i0) {
+    const int st = st0 + i0;
+    const bool in = i0 < count && st * 64 + piece * 8 < g.H;
+    const int so = i0 < count ? st * 128 : 0;
+    const uint32_t off = in ? off0 : kOob;
 #pragma unroll
-  for (int p = 0; p < PARTS; ++p)
-    ar[p] = make_rsrc(static_cast<const uint16_t*>(g.a) + p * g.plane + m0 * g.lda,
-                      int64_t(rows) * g.lda * 2);
-  const rsrc_t br = make_rsrc(static_cast<const uint16_t*>(g.b) + int64_t(n0) * g.ldb,
-                              int64_t(cols) * g.ldb * 2);
-  const int st0 = int(blockIdx.z) * g.each, st1 = st0 + g.each;
-  u32x4 av[D][PARTS][LOADS], bv[D][4][2];
-  auto load = [&](int d, int st) {
-    const int left = st < st1 ? g.K - st * (64 * WK) : 0;          // channels from the stage on
-    const int so = st < st1 ? st * (128 * WK) : 0;
+    for (int i = 0; i < LA; ++i)
+      av[d][i] = __builtin_amdgcn_raw_buffer_load_b128(ar, off + uint32_t(i) * step, so, 0);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-      const int at = i * kBlock + int(threadIdx.x), row = at / P, piece = at % P;
-      const uint32_t off = row < BM && piece * 8 < left
-                               ? uint32_t(row) * uint32_t(2 * g.lda) + uint32_t(piece * 16)
-                               : kOob;
+    for (int i = 0; i < LB; ++i)
+      bv[d][i] = __builtin_amdgcn_raw_buffer_load_b128(br, off + uint32_t(i) * step, so, 0);
+  };
+  auto write = [&](int d, int buf) {
+    u32x4* to = lds + buf * (kA + kB);
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p)
-        av[d][p][i] = __builtin_amdgcn_raw_buffer_load_b128(ar[p], off, so, 0);
-    }
+    for (int i = 0; i < LA; ++i)
+      if (kA % kBlock == 0 || int(threadIdx.x) + i * kBlock < kA) to[awrite + i * 256] = av[d][i];
+#pragma unroll
+    for (int i = 0; i < LB; ++i) to[bwrite + i * 256] = bv[d][i];
+  };
+  const int aread = (wm * 16 * MT + n) * 8, bread = kA + (wn * 64 + (n >> 2) * 16 + (n & 3)) * 8;
+  auto read = [&](int buf, int s, u32x4 (&a)[MT], u32x4 (&b)[4]) {
+    const u32x4* from = lds + buf * (kA + kB);
+    const int at = s * 4 + q;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
+      b[t] = from[bread + t * 32 + (at ^ ((n & 3) | (n & 4)))];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int piece = wk * 8 + s * 4 + q;
-        const uint32_t off = piece * 8 < left
-                                 ? uint32_t(wn * 64 + t * 16 + n) * uint32_t(2 * g.ldb) +
-                                       uint32_t(piece * 16)
-                                 : kOob;
-        bv[d][t][s] = __builtin_amdgcn_raw_buffer_load_b128(br, off, so, 0);
-      }
+    for (int m = 0; m < MT; ++m) a[m] = from[aread + m * 128 + (at ^ (n & 7))];
   };
   f32x4 acc[MT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 a0[MT], b0[4], a1[MT], b1[4];
+  auto products = [&](const u32x4 (&a)[MT], const u32x4 (&b)[4]) {
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(d, st0 + d);
-  for (int st = st0; st < st1; st += D) {
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
-      u32x4* buf = lds + (d & 1) * (PARTS * BM * P);
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        const int at = i * kBlock + int(threadIdx.x), row = at / P, piece = at % P;
-        if (row < BM) {
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p)
-            buf[(p * BM + row) * P + (piece ^ (row & 7))] = av[d][p][i];
-        }
-      }
-      u32x4 b[4][2];
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) b[t][s] = bv[d][t][s];
-      lds_barrier();
-      load(d, st + d + D);
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const int row = m * 16 + n;
-            const u32x4 a = buf[(p * BM + row) * P + ((wk * 8 + s * 4 + q) ^ (row & 7))];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) acc[m][t] = mfma(a, b[t][s], acc[m][t]);
-          }
-    }
-  }
-  const int64_t plane = int64_t(blockIdx.z) * g.M * g.N;
-  auto store = [&](int row, int col, float v) {
-    if (row >= rows || col >= cols) return;
-    const int64_t at = (m0 + row) * g.N + n0 + col;
-    if constexpr (BF16OUT)
-      static_cast<uint16_t*>(g.out)[at] = uint16_t(pack_bf16x2(v, 0.0f));
-    else
-      static_cast<float*>(g.out)[plane + at] = v;
+      for (int t = 0; t < 4; ++t) acc[m][t] = mfma(b[t], a[m], acc[m][t]);
   };
-  if constexpr (WK == 1) {
+  // stages 0 and 1 into LDS, 2 and on into the ring: stage i's place is i % R
+  load(0, 0);
+  load(1, 1);
+  load(2, 2);
+  write(0, 0);
+  load(0, 3);
+  write(1, 1);
+  load(1, 4);
+  lds_barrier();
+  read(0, 0, a0, b0);
+  for (int st = 0; st < count; st += 3) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          store(m * 16 + q * 4 + i, wn * 64 + t * 16 + n, acc[m][t][i]);
-  } else {
-    // the waves along k add up in order
-    float* sum = reinterpret_cast<float*>(lds);
-    lds_barrier();
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          sum[(wk * BM + m * 16 + q * 4 + i) * (64 * WN) + wn * 64 + t * 16 + n] = acc[m][t][i];
-    lds_barrier();
-    for (int at = int(threadIdx.x); at < BM * 64 * WN; at += kBlock) {
-      float v = 0.0f;
-#pragma unroll
-      for (int k = 0; k < WK; ++k) v += sum[k * (BM * 64 * WN) + at];
-      store(at / (64 * WN), at % (64 * WN), v);
+    for (int d = 0; d < 3; ++d) {
+      // stage st + d in buffer d; the next in (d + 1) % 3; d + 2 is written
+      read(d, 1, a1, b1);
+      products(a0, b0);
+      write((d + 2) % R, (d + 2) % 3);
+      load((d + 2) % R, st + d + 2 + R);
+      read((d + 1) % 3, 0, a0, b0);
+      products(a1, b1);
+      // a product, then one of the others, while there are any
+      interleave<MT * 4, MT + 4, LA + LB>();
+      lds_barrier();
     }
   }
-}
-
-// out[i] = sum over s of part[s][i], in order.
-__global__ __launch_bounds__(kBlock) void sum_planes_kernel(const float* part, int planes,
-                                                            int64_t count, float* out) {
-  const int64_t step = int64_t(gridDim.x) * kBlock;
-  for (int64_t i = int64_t(blockIdx.x) * kBlock + threadIdx.x; i < count; i += step) {
-    float v = 0.0f;
-    for (int s = 0; s < planes; ++s) v += part[s * count + i];
-    out[i] = v;
+  float* out = g.out + (int64_t(blockIdx.z) * g.T + m0) * g.E + n0;
+  const int col = wn * 64 + q * 16;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = (wm * MT + m) * 16 + n;
+    if (row >= rows || col >= cols) continue;
+    float* to = out + int64_t(row) * g.E + col;
+    if ((g.E & 3) == 0) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (col + 4 * t < cols) __builtin_memcpy(to + 4 * t, &acc[m][t], 16);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (col + 4 * t + i < cols) to[4 * t + i] = acc[m][t][i];
+    }
   }
 }
 
@@ -197,224 +209,341 @@ __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
   p[2] = pack_bf16x2(r - bf16_lo(p[1]), 0.0f) & 0xFFFFu;
 }
 
-constexpr int kTileSide = 64;
+__device__ __forceinline__ uint32_t half(uint32_t lo, uint32_t hi) { return lo | (hi << 16); }
 
-// A 64 x 64 tile of dlogits in parts: rows [2][T][Ep] and, transposed, columns
-// [3][Ep][Tp], zeros past its end.
-__global__ __launch_bounds__(kBlock) void split_kernel(const float* dl, int64_t T, int E,
-                                                       uint16_t* rows, uint16_t* columns) {
-  __shared__ float tile[kTileSide][kTileSide + 1];
-  const int64_t t0 = int64_t(blockIdx.x) * kTileSide;
-  const int e0 = int(blockIdx.y) * kTileSide;
-  const int64_t Ep = int64_t(gridDim.y) * kTileSide, Tp = int64_t(gridDim.x) * kTileSide;
-  const int c = int(threadIdx.x) & 63;
-  for (int r = int(threadIdx.x) >> 6; r < kTileSide; r += kBlock / 64)
-    tile[r][c] = t0 + r < T && e0 + c < E ? dl[(t0 + r) * E + e0 + c] : 0.0f;
-  __syncthreads();
-  for (int r = int(threadIdx.x) >> 6; r < kTileSide; r += kBlock / 64) {
-    uint32_t p[3];
-    if (rows && t0 + r < T) {
-      split3(tile[r][c], p);
+// ---------------------------------------------------------------------------
+// Operands of the gradients' products in the order in which the matrix cores
+// take them: blocks of 1 KB, 16 bytes a lane, lane (n, q) = (lane & 15, lane >> 4)
+// holding eight k of row n, k = 8 q and on of the block's 32.  A wave then loads
+// a block as one run of memory.  Row r of tile i stands for row
+// (r / 4) * 16 + i * 4 + r % 4 of 64 (wt), or i * 16 + r (columns).
+// ---------------------------------------------------------------------------
+
+// columns: dlogits transposed, [Ep / 64][Tp / 32][4 tiles][3 parts] blocks: rows
+// are experts, k tokens; zeros past their ends.  A thread makes the pieces of
+// eight tokens of an expert.
+__global__ __launch_bounds__(kBlock) void columns_kernel(const float* dl, int64_t T, int E, int Ep,
+                                                         u32x4* out, int64_t block0) {
+  const int64_t at = (block0 + blockIdx.x) * kBlock + threadIdx.x;
+  const int64_t t8 = at / Ep, T32 = (T + 31) / 32;
+  const int e = int(at - t8 * Ep);
+  if (t8 >= T32 * 4) return;
+  uint32_t p[8][3];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) rows[(i * T + t0 + r) * Ep + e0 + c] = uint16_t(p[i]);
+  for (int i = 0; i < 8; ++i)
+    split3(e < E && t8 * 8 + i < T ? dl[(t8 * 8 + i) * E + e] : 0.0f, p[i]);
+  const int64_t block = ((int64_t(e >> 6) * T32 + (t8 >> 2)) * 4 + ((e >> 4) & 3)) * 3;
+  const int lane = int(t8 & 3) * 16 + (e & 15);
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    out[(block + j) * kWave + lane] = u32x4{half(p[0][j], p[1][j]), half(p[2][j], p[3][j]),
+                                            half(p[4][j], p[5][j]), half(p[6][j], p[7][j])};
+}
+
+// wt: the weights transposed, [Hp / 64][Ep / 32][4 tiles] blocks: rows are
+// channels, k experts; zeros past their ends.
+__global__ __launch_bounds__(kBlock) void wt_kernel(const uint16_t* w, int E, int H, int Ep,
+                                                    int64_t Hp, u32x4* out) {
+  const int64_t at = int64_t(blockIdx.x) * kBlock + threadIdx.x;
+  const int e8 = int(at / Hp);
+  const int64_t h = at - e8 * Hp;
+  if (e8 * 8 >= Ep) return;
+  uint32_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = h < H && e8 * 8 + i < E ? w[int64_t(e8 * 8 + i) * H + h] : 0u;
+  const int r = int(h & 3) | int((h >> 4) & 3) << 2, tile = int(h >> 2) & 3;
+  out[(((h >> 6) * (Ep >> 5) + (e8 >> 2)) * 4 + tile) * kWave + (e8 & 3) * 16 + r] =
+      u32x4{half(v[0], v[1]), half(v[2], v[3]), half(v[4], v[5]), half(v[6], v[7])};
+}
+
+// ---------------------------------------------------------------------------
+// dx[t, h] = sum over e of dlogits[t, e] w[e, h].  A workgroup keeps its 16 MT
+// tokens' rows of dlogits in LDS, as two bf16 parts in the order above, and
+// walks along the channels: each wave streams its share of wt, 64 channels at a
+// time, and stores 16 neighbouring channels of a token a lane.
+// ---------------------------------------------------------------------------
+struct DxArgs {
+  const float* dl;
+  const u32x4* wt;
+  int64_t T;
+  int E, Ep, H;
+  int each;                      // blocks of 64 channels a workgroup takes
+  void* dx;
+};
+
+template <int MT>
+__global__ __launch_bounds__(kBlock) void dx_kernel(DxArgs g, int64_t mb0) {
+  extern __shared__ u32x4 rows[];            // [2 parts][Ep / 32][MT] blocks
+  const int lane = lane_id(), n = lane & 15, q = lane >> 4;
+  const int64_t m0 = (mb0 + blockIdx.x) * (16 * MT);
+  const int K32 = g.Ep >> 5, E8 = g.Ep >> 3;
+  const int part = K32 * MT * kWave;
+  for (int at = int(threadIdx.x); at < 16 * MT * E8; at += kBlock) {
+    const int r = at / E8, e = (at - r * E8) * 8;
+    float v[8];
+    const float* from = g.dl + (m0 + r) * g.E + e;
+    const int left = m0 + r < g.T ? g.E - e : 0;
+    if ((g.E & 3) == 0 && left >= 8) {
+      __builtin_memcpy(v, __builtin_assume_aligned(from, 4), 32);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < left ? from[i] : 0.0f;
     }
-    if (columns) {
-      split3(tile[c][r], p);
+    uint32_t p[8][3];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) columns[(i * Ep + e0 + r) * Tp + t0 + c] = uint16_t(p[i]);
+    for (int i = 0; i < 8; ++i) split3(v[i], p[i]);
+    const int to = ((e >> 5) * MT + (r >> 4)) * kWave + ((e >> 3) & 3) * 16 + (r & 15);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      rows[j * part + to] = u32x4{half(p[0][j], p[1][j]), half(p[2][j], p[3][j]),
+                                  half(p[4][j], p[5][j]), half(p[6][j], p[7][j])};
+  }
+  __syncthreads();
+  // this wave's blocks of 64 channels
+  const int all = (g.H + 63) >> 6;
+  const int first = int(blockIdx.y) * g.each;
+  const int end = first + g.each < all ? first + g.each : all;
+  const int share = (end - first + 3) / 4;
+  const int hb0 = first + wave_id() * share;
+  const int hb1 = hb0 + share < end ? hb0 + share : end;
+  if (hb0 >= hb1) return;
+  const int pairs = K32 >> 1;                // steps of 64 experts a block
+  const int64_t total = int64_t(hb1 - hb0) * pairs;
+  const u32x4* w = g.wt + int64_t(hb0) * K32 * (4 * kWave) + lane;
+  u32x4 b[2][2][4];
+  auto load = [&](int d, int64_t p) {
+    if (p >= total) return;                  // the same for the whole wave
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) b[d][s][t] = w[((p * 2 + s) * 4 + t) * kWave];
+  };
+  f32x4 acc[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  load(0, 0);
+  load(1, 1);
+  int k = 0, hb = hb0;
+  for (int64_t p0 = 0; p0 < total; p0 += 2) {
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      if (p0 + d >= total) break;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const u32x4 a = rows[j * part + ((2 * k + s) * MT + m) * kWave + lane];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) acc[m][t] = mfma(b[d][s][t], a, acc[m][t]);
+          }
+      load(d, p0 + d + 2);
+      if (++k < pairs) continue;
+      const int h = hb * 64 + q * 16;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int64_t t = m0 + m * 16 + n;
+        u32x4* to = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.dx) + t * g.H + h);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (t < g.T && h + 8 * i < g.H)
+            to[i] = u32x4{pack_bf16x2(acc[m][2 * i][0], acc[m][2 * i][1]),
+                          pack_bf16x2(acc[m][2 * i][2], acc[m][2 * i][3]),
+                          pack_bf16x2(acc[m][2 * i + 1][0], acc[m][2 * i + 1][1]),
+                          pack_bf16x2(acc[m][2 * i + 1][2], acc[m][2 * i + 1][3])};
+#pragma unroll
+        for (int t4 = 0; t4 < 4; ++t4) acc[m][t4] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      k = 0;
+      ++hb;
     }
   }
 }
 
-// w [E][H] to [H][Ep], zeros past E.
-__global__ __launch_bounds__(kBlock) void transpose_kernel(const uint16_t* w, int E, int H,
-                                                           uint16_t* wt) {
-  __shared__ uint16_t tile[kTileSide][kTileSide + 2];
-  const int h0 = int(blockIdx.x) * kTileSide, e0 = int(blockIdx.y) * kTileSide;
-  const int64_t Ep = int64_t(gridDim.y) * kTileSide;
-  const int c = int(threadIdx.x) & 63;
-  for (int r = int(threadIdx.x) >> 6; r < kTileSide; r += kBlock / 64)
-    tile[r][c] = e0 + r < E && h0 + c < H ? w[int64_t(e0 + r) * H + h0 + c] : uint16_t(0);
-  __syncthreads();
-  for (int r = int(threadIdx.x) >> 6; r < kTileSide; r += kBlock / 64)
-    if (h0 + r < H) wt[int64_t(h0 + r) * Ep + e0 + c] = tile[c][r];
-}
-
-struct OuterArgs {
-  const void* d;                 // [3][Ep][Tp] bf16
+// ---------------------------------------------------------------------------
+// dw[e, h] = sum over t of dlogits[t, e] x[t, h].  A workgroup takes 64 experts
+// and 128 channels, its waves every fourth step of 32 tokens; they add up at the
+// end, in order.  The sum runs along the rows of x, so a fragment needs eight
+// tokens of one channel in a lane: lane n loads eight neighbouring channels 8n..
+// of eight rows, 256 bytes of a row at a time, and swaps halves of words;
+// fragment c then holds the channels 8n + c, and a lane's results are neighbours.
+// ---------------------------------------------------------------------------
+struct DwArgs {
+  const u32x4* columns;
   const void* x;                 // [T][H] bf16
-  int64_t T, Tp;
-  int E, Ep, H;
+  int64_t T;
+  int E, H;
   int64_t each;                  // steps of 32 tokens a workgroup takes
   float* out;                    // [splits][E][H]
 };
 
-// ---------------------------------------------------------------------------
-// dw[e, h] = sum over t of D[e, t] x[t, h], D the sum of three bf16 arrays.  A
-// wave takes 64 experts and 64 channels.  The sum runs along the rows of x, so
-// a fragment needs eight tokens of one channel in a lane: lane n loads four
-// neighbouring channels 4n.. of eight rows, 128 bytes of a row at a time, and
-// swaps halves of words; fragment c then holds the channels 4n + c.
-// ---------------------------------------------------------------------------
-__global__ __launch_bounds__(kBlock) void outer_kernel(OuterArgs g) {
-  const int lane = lane_id(), n = lane & 15, q = lane >> 4;
-  const int h0 = int(blockIdx.x) * 256 + wave_id() * 64 + n * 4;
+__global__ __launch_bounds__(kBlock, 1) void dw_kernel(DwArgs g) {
+  constexpr int kPitch = 132;                // floats a row of sums
+  __shared__ float sum[4][64][kPitch];
+  const int lane = lane_id(), n = lane & 15, q = lane >> 4, wave = wave_id();
+  const int h0 = int(blockIdx.x) * 128;
   const int e0 = int(blockIdx.y) * 64;
+  const int64_t T32 = (g.T + 31) / 32;
   const int64_t s0 = int64_t(blockIdx.z) * g.each;
-  const int64_t steps = (g.T + 31) / 32;
-  const int64_t s1 = s0 + g.each < steps ? s0 + g.each : steps;
-  f32x4 acc[4][4];
+  const int64_t s1 = s0 + g.each < T32 ? s0 + g.each : T32;
+  const u32x4* columns = g.columns + int64_t(blockIdx.y) * T32 * (12 * kWave) + lane;
+  const uint32_t pitch = uint32_t(2 * g.H);
+  const uint32_t off = h0 + n * 8 < g.H ? uint32_t(q * 8) * pitch + uint32_t(2 * (h0 + n * 8))
+                                        : kOob;
+  u32x4 a[12], v[8];
+  auto load = [&](int64_t s) {
+    if (s >= s1) return;                     // the same for the whole wave
+#pragma unroll
+    for (int i = 0; i < 12; ++i) a[i] = columns[(s * 12 + i) * kWave];
+    const int64_t left = g.T - s * 32;
+    const rsrc_t xr = make_rsrc(static_cast<const uint16_t*>(g.x) + s * 32 * g.H,
+                                (left < 32 ? left : 32) * pitch);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = __builtin_amdgcn_raw_buffer_load_b128(xr, off + uint32_t(i) * pitch, 0, 0);
+  };
+  f32x4 acc[4][8];
 #pragma unroll
   for (int m = 0; m < 4; ++m)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const uint16_t* d = static_cast<const uint16_t*>(g.d) + int64_t(e0 + n) * g.Tp + q * 8;
-  const uint16_t* x = static_cast<const uint16_t*>(g.x) + h0;
-  for (int64_t s = s0; s < s1; ++s) {
-    const int64_t t0 = s * 32 + q * 8;
-    u32x2 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = u32x2{0u, 0u};
-      if (h0 < g.H && t0 + i < g.T) v[i] = *reinterpret_cast<const u32x2*>(x + (t0 + i) * g.H);
-    }
-    u32x4 b[4];
+    for (int c = 0; c < 8; ++c) acc[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  load(s0 + wave);
+  for (int64_t s = s0 + wave; s < s1; s += 4) {
+    u32x4 b[8], d[12];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
+      for (int w = 0; w < 4; ++w) {
         b[2 * w][i] = __builtin_amdgcn_perm(v[2 * i + 1][w], v[2 * i][w], 0x05040100u);
         b[2 * w + 1][i] = __builtin_amdgcn_perm(v[2 * i + 1][w], v[2 * i][w], 0x07060302u);
       }
 #pragma unroll
+    for (int i = 0; i < 12; ++i) d[i] = a[i];
+    load(s + 4);
+#pragma unroll
     for (int p = 0; p < 3; ++p)
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const u32x4 a = *reinterpret_cast<const u32x4*>(
-            d + (int64_t(p) * g.Ep + m * 16) * g.Tp + s * 32);
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[m][c] = mfma(a, b[c], acc[m][c]);
-      }
+        for (int c = 0; c < 8; ++c) acc[m][c] = mfma(d[m * 3 + p], b[c], acc[m][c]);
   }
-  float* out = g.out + int64_t(blockIdx.z) * g.E * g.H;
-  if (h0 >= g.H) return;
 #pragma unroll
   for (int m = 0; m < 4; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = e0 + m * 16 + q * 4 + i;
-      if (e < g.E)
-        *reinterpret_cast<f32x4*>(out + int64_t(e) * g.H + h0) =
-            f32x4{acc[m][0][i], acc[m][1][i], acc[m][2][i], acc[m][3][i]};
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<f32x4*>(&sum[wave][m * 16 + q * 4 + i][n * 8 + 4 * j]) =
+            f32x4{acc[m][4 * j][i], acc[m][4 * j + 1][i], acc[m][4 * j + 2][i],
+                  acc[m][4 * j + 3][i]};
+  __syncthreads();
+  float* out = g.out + int64_t(blockIdx.z) * g.E * g.H;
+  for (int at = int(threadIdx.x); at < 64 * 32; at += kBlock) {
+    const int r = at >> 5, c = (at & 31) * 4;
+    if (e0 + r >= g.E || h0 + c >= g.H) continue;
+    f32x4 t = *reinterpret_cast<const f32x4*>(&sum[0][r][c]);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) t += *reinterpret_cast<const f32x4*>(&sum[w][r][c]);
+    *reinterpret_cast<f32x4*>(out + int64_t(e0 + r) * g.H + h0 + c) = t;
+  }
 }
 
-template <int MT, int WN, int PARTS, bool BF16OUT>
-void launch_gemm_shape(const GemmArgs& g, const GemmShape& s, hipStream_t stream) {
+template <int MT, int WM, int WN>
+void launch_logits_shape(const LogitsGemm& g, const LogitsShape& s, hipStream_t stream) {
   const int64_t most = max_blocks(kBlock) / (int64_t(s.nb) * s.splits);
   for (int64_t b0 = 0; b0 < s.mb; b0 += most) {
     const dim3 grid{unsigned(s.mb - b0 < most ? s.mb - b0 : most), unsigned(s.nb),
                     unsigned(s.splits)};
-    gemm_kernel<MT, WN, PARTS, BF16OUT><<<grid, kBlock, 0, stream>>>(g, b0);
+    logits_kernel<MT, WM, WN><<<grid, kBlock, 0, stream>>>(g, b0);
   }
 }
 
-template <int PARTS, bool BF16OUT>
-void launch_gemm(const GemmArgs& g, const GemmShape& s, hipStream_t stream) {
-  if (s.mt == 1) {
-    if (s.wn == 1)
-      launch_gemm_shape<1, 1, PARTS, BF16OUT>(g, s, stream);
-    else if (s.wn == 2)
-      launch_gemm_shape<1, 2, PARTS, BF16OUT>(g, s, stream);
-    else
-      launch_gemm_shape<1, 4, PARTS, BF16OUT>(g, s, stream);
-  } else if (s.mt == 2) {
-    if (s.wn == 1)
-      launch_gemm_shape<2, 1, PARTS, BF16OUT>(g, s, stream);
-    else if (s.wn == 2)
-      launch_gemm_shape<2, 2, PARTS, BF16OUT>(g, s, stream);
-    else
-      launch_gemm_shape<2, 4, PARTS, BF16OUT>(g, s, stream);
-  } else {
-    if (s.wn == 1)
-      launch_gemm_shape<4, 1, PARTS, BF16OUT>(g, s, stream);
-    else if (s.wn == 2)
-      launch_gemm_shape<4, 2, PARTS, BF16OUT>(g, s, stream);
-    else
-      launch_gemm_shape<4, 4, PARTS, BF16OUT>(g, s, stream);
+template <int MT>
+void launch_dx(const DxArgs& g, const DxShape& s, hipStream_t stream) {
+  const unsigned lds = unsigned(2 * 16 * MT * g.Ep * 2);
+  const int64_t most = max_blocks(kBlock) / s.splits;
+  for (int64_t b0 = 0; b0 < s.mb; b0 += most) {
+    const dim3 grid{unsigned(s.mb - b0 < most ? s.mb - b0 : most), unsigned(s.splits), 1u};
+    dx_kernel<MT><<<grid, kBlock, lds, stream>>>(g, b0);
   }
-}
-
-void launch_sum_planes(const float* part, int planes, int64_t count, float* out, hipStream_t s) {
-  const int64_t blocks = (count + kBlock - 1) / kBlock;
-  sum_planes_kernel<<<unsigned(blocks < (1 << 20) ? blocks : (1 << 20)), kBlock, 0, s>>>(
-      part, planes, count, out);
 }
 
 }  // namespace
 
 hipError_t launch_router_logits(const LogitsArgs& a, hipStream_t s) {
-  const GemmShape shape = gemm_shape(a.T, a.E, a.H, true);
-  GemmArgs g{};
-  g.a = a.x;
-  g.b = a.w;
-  g.M = a.T;
-  g.N = a.E;
-  g.K = a.H;
-  g.lda = g.ldb = a.H;
+  const LogitsShape shape = logits_shape(a.T, a.E, a.H);
+  LogitsGemm g{};
+  g.x = a.x;
+  g.w = a.w;
+  g.T = a.T;
+  g.E = a.E;
+  g.H = a.H;
   g.each = shape.each;
-  g.out = shape.splits > 1 ? a.ws : static_cast<void*>(a.logits);
-  launch_gemm<1, false>(g, shape, s);
+  g.out = shape.splits > 1 ? static_cast<float*>(a.ws) : a.logits;
+  if (shape.bm == 16)
+    launch_logits_shape<1, 1, 4>(g, shape, s);
+  else if (shape.bm == 32)
+    launch_logits_shape<2, 1, 4>(g, shape, s);
+  else if (shape.wn == 1)
+    launch_logits_shape<1, 4, 1>(g, shape, s);
+  else if (shape.wn == 2)
+    launch_logits_shape<2, 2, 2>(g, shape, s);
+  else
+    launch_logits_shape<4, 1, 4>(g, shape, s);
   if (shape.splits > 1)
-    launch_sum_planes(static_cast<const float*>(a.ws), shape.splits, a.T * a.E, a.logits, s);
+    launch_sum_rows(static_cast<const float*>(a.ws), shape.splits, a.T * a.E, a.logits, s);
   return hipGetLastError();
 }
 
 hipError_t launch_router_logits_backward(const LogitsArgs& a, hipStream_t s) {
   const LogitsBackwardSpace at = logits_backward_space(a.T, a.E, a.H);
   char* ws = static_cast<char*>(a.ws);
-  uint16_t* rows = reinterpret_cast<uint16_t*>(ws + at.rows);
-  uint16_t* columns = reinterpret_cast<uint16_t*>(ws + at.columns);
-  uint16_t* wt = reinterpret_cast<uint16_t*>(ws + at.wt);
+  u32x4* columns = reinterpret_cast<u32x4*>(ws + at.columns);
+  u32x4* wt = reinterpret_cast<u32x4*>(ws + at.wt);
   const int Ep = int(pad64(a.E));
-  const int64_t Tp = pad64(a.T);
-  if (a.T > 0) {
-    const dim3 grid{unsigned(Tp / kTileSide), unsigned(Ep / kTileSide), 1u};
-    split_kernel<<<grid, kBlock, 0, s>>>(a.dlogits, a.T, a.E, a.dx ? rows : nullptr,
-                                         a.dw ? columns : nullptr);
-  }
   if (a.dx) {
-    const dim3 grid{unsigned((a.H + kTileSide - 1) / kTileSide), unsigned(Ep / kTileSide), 1u};
-    transpose_kernel<<<grid, kBlock, 0, s>>>(static_cast<const uint16_t*>(a.w), a.E, a.H, wt);
-    const GemmShape shape = gemm_shape(a.T, a.H, Ep, false);
-    GemmArgs g{};
-    g.a = rows;
-    g.b = wt;
-    g.M = a.T;
-    g.N = a.H;
-    g.K = Ep;
-    g.lda = g.ldb = Ep;
-    g.plane = a.T * Ep;
-    g.each = shape.each;
-    g.out = a.dx;
-    launch_gemm<2, true>(g, shape, s);
-  }
-  if (a.dw) {
-    const OuterShape o = outer_shape(a.T, a.E, a.H);
-    OuterArgs g{};
-    g.d = columns;
-    g.x = a.x;
+    const int64_t Hp = pad64(a.H);
+    wt_kernel<<<unsigned((Hp * (Ep / 8) + kBlock - 1) / kBlock), kBlock, 0, s>>>(
+        static_cast<const uint16_t*>(a.w), a.E, a.H, Ep, Hp, wt);
+    const DxShape shape = dx_shape(a.T, a.H, Ep);
+    DxArgs g{};
+    g.dl = a.dlogits;
+    g.wt = wt;
     g.T = a.T;
-    g.Tp = Tp;
     g.E = a.E;
     g.Ep = Ep;
     g.H = a.H;
-    g.each = o.each;
-    g.out = o.splits > 1 ? reinterpret_cast<float*>(ws + at.part) : a.dw;
-    const dim3 grid{unsigned(o.hb), unsigned(o.eb), unsigned(o.splits)};
-    outer_kernel<<<grid, kBlock, 0, s>>>(g);
-    if (o.splits > 1)
-      launch_sum_planes(g.out, o.splits, int64_t(a.E) * a.H, a.dw, s);
+    g.each = shape.each;
+    g.dx = a.dx;
+    if (shape.mt == 1)
+      launch_dx<1>(g, shape, s);
+    else if (shape.mt == 2)
+      launch_dx<2>(g, shape, s);
+    else
+      launch_dx<4>(g, shape, s);
+  }
+  if (a.dw) {
+    const int64_t pieces = (a.T + 31) / 32 * 4 * Ep;
+    for_each_launch((pieces + kBlock - 1) / kBlock, kBlock, [&](int64_t b0, unsigned grid) {
+      columns_kernel<<<grid, kBlock, 0, s>>>(a.dlogits, a.T, a.E, Ep, columns, b0);
+    });
+    const DwShape shape = dw_shape(a.T, a.E, a.H);
+    DwArgs g{};
+    g.columns = columns;
+    g.x = a.x;
+    g.T = a.T;
+    g.E = a.E;
+    g.H = a.H;
+    g.each = shape.each;
+    g.out = shape.splits > 1 ? reinterpret_cast<float*>(ws + at.part) : a.dw;
+    const dim3 grid{unsigned(shape.hb), unsigned(shape.eb), unsigned(shape.splits)};
+    dw_kernel<<<grid, kBlock, 0, s>>>(g);
+    if (shape.splits > 1)
+      launch_sum_rows(g.out, shape.splits, int64_t(a.E) * a.H, a.dw, s);
   }
   return hipGetLastError();
 }

@@ -1,6 +1,6 @@
 // RMS norm with the residual's addition and an 8-bit output, and its gradient
 // (gfx950, wave64).  A few operations a byte: HBM bounds both.
-#include "epdc_device.h"
+#include "router_device.h"
 #include "router_launch.h"
 
 namespace epdc {
@@ -238,42 +238,6 @@ __global__ __launch_bounds__(kNormMaxWaves* kWave) void rms_norm_backward_kernel
   }
 }
 
-// Sum of `rows` rows of partial sums: a workgroup takes 64 columns, 16 threads
-// of four columns each, 16 of them side by side over the rows.
-constexpr int kSumColumns = 64;
-__global__ __launch_bounds__(kBlock) void sum_rows_kernel(const float* part, int rows, int H,
-                                                          float* out) {
-  __shared__ float4 acc[16][16];
-  const int cx = int(threadIdx.x) & 15, ry = int(threadIdx.x) >> 4;
-  const int c = int(blockIdx.x) * kSumColumns + cx * 4;
-  float4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < H) {
-    for (int r = ry; r < rows; r += 16) {
-      const float4 v = *reinterpret_cast<const float4*>(part + int64_t(r) * H + c);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-  }
-  acc[ry][cx] = s;
-  __syncthreads();
-  if (ry != 0 || c >= H) return;
-#pragma unroll
-  for (int r = 1; r < 16; ++r) {
-    const float4 v = acc[r][cx];
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
-  }
-  // dweight may be 4-byte aligned only
-  out[c] = s.x;
-  out[c + 1] = s.y;
-  out[c + 2] = s.z;
-  out[c + 3] = s.w;
-}
-
 template <bool W32>
 void launch_norm_w(const NormArgs& a, hipStream_t s) {
   const NormShape n = norm_shape(a.H);
@@ -318,8 +282,7 @@ hipError_t launch_rms_norm_backward(const NormArgs& a, hipStream_t s) {
   else if (g > 0)
     launch_norm_backward_w<false>(a, g, s);
   if (a.dweight)                            // zeros for no rows
-    sum_rows_kernel<<<unsigned((a.H + kSumColumns - 1) / kSumColumns), kBlock, 0, s>>>(
-        a.part, int(g), a.H, a.dweight);
+    launch_sum_rows(a.part, int(g), a.H, a.dweight, s);
   return hipGetLastError();
 }
 

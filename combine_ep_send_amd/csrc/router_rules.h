@@ -52,27 +52,24 @@ inline RouteShape route_shape(int E, int groups) {
 }
 
 // ---- the router's products -----------------------------------------------------
-// out[m, n] = sum over k of A[m, k] B[n, k]: a workgroup takes 16 * mt rows of A
-// and 64 * wn rows of B; its four waves are wn side by side along n times
-// 4 / wn along k, and a stage is 64 channels k for each of the latter.  The
-// stages are split over `splits` workgroups, `each` a workgroup.
-struct GemmShape {
-  int mt, wn;
+constexpr int kGemmGroups = 256;      // workgroups that fill the chip
+
+// Logits: a workgroup takes bm tokens and 64 * wn experts over `each` stages of
+// 64 channels.
+struct LogitsShape {
+  int bm, wn;
   int64_t mb;
   int nb, splits, each;
 };
 
-constexpr int kGemmGroups = 256;      // workgroups that fill the chip
-
-inline GemmShape gemm_shape(int64_t M, int N, int K, bool splittable) {
-  GemmShape g{};
-  g.mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  g.mb = M > 0 ? (M + 16 * g.mt - 1) / (16 * g.mt) : 1;
-  g.wn = N <= 64 || g.mb * ((N + 63) / 64) < kGemmGroups ? 1 : N <= 128 ? 2 : 4;
-  g.nb = (N + 64 * g.wn - 1) / (64 * g.wn);
-  const int depth = 64 * (4 / g.wn);
-  const int stages = (K + depth - 1) / depth;
-  int64_t want = splittable ? kGemmGroups / (g.mb * g.nb) : 1;
+inline LogitsShape logits_shape(int64_t T, int E, int H) {
+  LogitsShape g{};
+  g.bm = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  g.mb = T > 0 ? (T + g.bm - 1) / g.bm : 1;
+  g.wn = g.bm < 64 ? 4 : E <= 64 ? 1 : E <= 128 ? 2 : 4;
+  g.nb = (E + 64 * g.wn - 1) / (64 * g.wn);
+  const int stages = (H + 63) / 64;
+  int64_t want = kGemmGroups / (g.mb * g.nb);
   if (want < 1) want = 1;
   if (want > stages) want = stages;
   g.each = int((stages + want - 1) / want);
@@ -80,54 +77,72 @@ inline GemmShape gemm_shape(int64_t M, int N, int K, bool splittable) {
   return g;
 }
 
-// The weights' gradient: a workgroup takes 64 experts and 256 channels (64 a
-// wave) over `each` steps of 32 tokens.
-struct OuterShape {
+// The rows' gradient: a workgroup keeps 16 * mt tokens' rows of dlogits in LDS,
+// 64 KB of them, and takes `each` blocks of 64 channels.
+struct DxShape {
+  int mt;
+  int64_t mb;
+  int splits, each;
+};
+
+inline DxShape dx_shape(int64_t T, int H, int Ep) {
+  DxShape d{};
+  const int most = Ep <= 256 ? 4 : Ep <= 512 ? 2 : 1;
+  const int fit = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  d.mt = most < fit ? most : fit;
+  d.mb = (T + 16 * d.mt - 1) / (16 * d.mt);
+  const int blocks = (H + 63) / 64;
+  int64_t want = 2 * kGemmGroups / (d.mb > 0 ? d.mb : 1);
+  if (want > (blocks + 3) / 4) want = (blocks + 3) / 4;
+  if (want < 1) want = 1;
+  d.each = int((blocks + want - 1) / want);
+  d.splits = (blocks + d.each - 1) / d.each;
+  return d;
+}
+
+// The weights' gradient: a workgroup takes 64 experts and 128 channels over
+// `each` steps of 32 tokens.
+struct DwShape {
   int eb, hb, splits;
   int64_t each;
 };
 
-inline OuterShape outer_shape(int64_t T, int E, int H) {
-  OuterShape o{};
-  o.eb = (E + 63) / 64;
-  o.hb = (H + 255) / 256;
+inline DwShape dw_shape(int64_t T, int E, int H) {
+  DwShape d{};
+  d.eb = (E + 63) / 64;
+  d.hb = (H + 127) / 128;
   const int64_t steps = (T + 31) / 32;
-  int64_t want = 512 / (int64_t(o.eb) * o.hb);
-  if (want > 64) want = 64;
+  int64_t want = kGemmGroups / (int64_t(d.eb) * d.hb);
   if (want > steps / 4) want = steps / 4;
   if (want < 1) want = 1;
-  o.each = (steps + want - 1) / want;
-  if (o.each < 1) o.each = 1;
-  o.splits = steps ? int((steps + o.each - 1) / o.each) : 1;
-  return o;
+  d.each = steps ? (steps + want - 1) / want : 1;
+  d.splits = steps ? int((steps + d.each - 1) / d.each) : 1;
+  return d;
 }
 
-// Workspaces.  Padded sizes: experts and tokens to 64.
+// Workspaces.
 inline int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 
 inline size_t logits_ws_bytes(int64_t T, int E, int H) {
-  const GemmShape g = gemm_shape(T, E, H, true);
+  const LogitsShape g = logits_shape(T, E, H);
   return 256 + (g.splits > 1 ? size_t(g.splits) * size_t(T) * size_t(E) * 4 : 0);
 }
 
 struct LogitsBackwardSpace {
-  size_t rows;       // dlogits in two bf16 parts [2][T][Ep]
-  size_t columns;    // in three, transposed [3][Ep][Tp]
-  size_t wt;         // the weights transposed [H][Ep]
+  size_t columns;    // dlogits transposed, in three bf16 parts
+  size_t wt;         // the weights transposed
   size_t part;       // partial sums of dw [splits][E][H] fp32
   size_t total;
 };
 
 inline LogitsBackwardSpace logits_backward_space(int64_t T, int E, int H) {
-  const size_t Ep = size_t(pad64(E)), Tp = size_t(pad64(T));
-  const OuterShape o = outer_shape(T, E, H);
-  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  const size_t Ep = size_t(pad64(E));
+  const DwShape d = dw_shape(T, E, H);
   LogitsBackwardSpace s{};
-  s.rows = 0;
-  s.columns = s.rows + up(4 * size_t(T) * Ep);
-  s.wt = s.columns + up(6 * Tp * Ep);
-  s.part = s.wt + up(2 * size_t(H) * Ep);
-  s.total = s.part + (o.splits > 1 ? size_t(o.splits) * size_t(E) * size_t(H) * 4 : 0) + 256;
+  s.columns = 0;
+  s.wt = s.columns + 6 * Ep * ((size_t(T) + 31) / 32 * 32);
+  s.part = s.wt + 2 * Ep * size_t(pad64(H));
+  s.total = s.part + (d.splits > 1 ? size_t(d.splits) * size_t(E) * size_t(H) * 4 : 0) + 256;
   return s;
 }
 
