@@ -18,22 +18,27 @@ namespace epdc {
 
 namespace {
 
-// Below every key: those come from fp32 sums, and infinite ones are cut to
-// kLargest.
+// kNone: no key.  Every key lies above kLowest, since keys come from fp32 sums and
+// infinite ones are cut to kLargest; kNone lies below it with any number in its
+// last bits.
 constexpr double kNone = -1.7e308;
+constexpr double kLowest = -1.6e308;
 constexpr double kLargest = 1.0e300;
-constexpr uint64_t kIndexBits = 1023;
+constexpr uint32_t kIndexBits = 1023;
 static_assert(kIndexBits >= 1024 - 1, "an expert's number fits");
 
 __device__ __forceinline__ double key_of(double v, int e) {
   // +0.0 turns -0 into +0, which are equal
-  uint64_t b = __builtin_bit_cast(uint64_t, fmin(v, kLargest) + 0.0) & ~kIndexBits;
-  b |= (b >> 63) ? uint64_t(e) : kIndexBits - uint64_t(e);
-  return __builtin_bit_cast(double, b);
+  const uint64_t b = __builtin_bit_cast(uint64_t, fmin(v, kLargest) + 0.0);
+  const uint32_t hi = uint32_t(b >> 32);
+  // the larger code for the lower number; a negative key's the other way round
+  const uint32_t code = uint32_t(kIndexBits - e) ^ (uint32_t(int32_t(hi) >> 31) & kIndexBits);
+  const uint32_t lo = (uint32_t(b) & ~kIndexBits) | code;
+  return __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
 }
 __device__ __forceinline__ int expert_of(double key) {
   const uint64_t b = __builtin_bit_cast(uint64_t, key);
-  const int c = int(b & kIndexBits);
+  const int c = int(uint32_t(b) & kIndexBits);
   return (b >> 63) ? c : int(kIndexBits) - c;
 }
 
@@ -128,6 +133,41 @@ __device__ __forceinline__ void join(const double (&v)[N], double (&out)[KP]) {
   }
 }
 
+// The two largest of the lists (b0, b1) of a group's `width` lanes.
+template <int LANES, int STEP = 0>
+__device__ __forceinline__ void best_two(double& b0, double& b1, int width) {
+  if constexpr ((1 << STEP) < LANES) {
+    if ((1 << STEP) >= width) return;
+    const double c0 = partner<STEP>(b0), c1 = partner<STEP>(b1);
+    b1 = fmax(fmin(b0, c0), fmax(b1, c1));
+    b0 = fmax(b0, c0);
+    best_two<LANES, STEP + 1>(b0, b1, width);
+  }
+}
+
+// How many of the token's lanes hold more than v.
+template <int TURN>
+__device__ __forceinline__ int turned_lanes(double v) {
+  if constexpr (TURN < 16) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(
+        int(uint32_t(b)), int(uint32_t(b)), 0x120 + TURN, 0xF, 0xF, false));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(
+        int(uint32_t(b >> 32)), int(uint32_t(b >> 32)), 0x120 + TURN, 0xF, 0xF, false));
+    return (__builtin_bit_cast(double, (uint64_t(hi) << 32) | lo) > v ? 1 : 0) +
+           turned_lanes<TURN + 1>(v);
+  }
+  return 0;
+}
+template <int LANES>
+__device__ __forceinline__ int better_lanes(double v) {
+  if constexpr (LANES == 16) return turned_lanes<1>(v);
+  int n = 0;
+  for (int i = 1; i < LANES; ++i)
+    n += from_lane(v, (lane_id() & ~(LANES - 1)) | ((lane_id() + i) & (LANES - 1))) > v ? 1 : 0;
+  return n;
+}
+
 // The largest KP (or all PER) of a lane's keys, descending.
 template <int KP, int PER>
 struct Local {
@@ -150,22 +190,58 @@ struct Local {
   }
 };
 
-// exp(-|l|) and from it the sigmoid, without cancellation on either side.
+// exp(x) for -800 <= x <= 0 (64 bits hold no less than exp(-745)), NaN for NaN:
+// Cody and Waite's reduction x = n ln 2 + r with |r| <= ln 2 / 2, ln 2 in two parts
+// of which n times the first is exact, and the Taylor polynomial of degree 12 of
+// exp(r), whose remainder is below 2^-52.
+__device__ __forceinline__ double exp_within(double x) {
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  double r = __builtin_fma(n, -0x1.62e42feep-1, x);
+  r = __builtin_fma(n, -0x1.a39ef35793c76p-33, r);
+  constexpr double kInverse[13] = {1.0,         1.0,          1.0 / 2,       1.0 / 6,
+                                   1.0 / 24,    1.0 / 120,    1.0 / 720,     1.0 / 5040,
+                                   1.0 / 40320, 1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800,
+                                   1.0 / 479001600};
+  double p = kInverse[12];
+#pragma unroll
+  for (int i = 11; i >= 0; --i) p = __builtin_fma(p, r, kInverse[i]);
+  return __builtin_amdgcn_ldexp(p, int(n));
+}
+// The same for any x <= 0.
+__device__ __forceinline__ double exp_down(double x) {
+  return exp_within(x < -800.0 ? -800.0 : x);
+}
+// 1 / y for y in [1, 2]: the hardware's estimate and two of Newton's steps.
+__device__ __forceinline__ double inverse(double y) {
+  double r = __builtin_amdgcn_rcp(y);
+  r = __builtin_fma(r, __builtin_fma(-y, r, 1.0), r);
+  return __builtin_fma(r, __builtin_fma(-y, r, 1.0), r);
+}
+
+// From exp(-|l|), without cancellation on either side.  The first is for logits
+// that are no NaN.
+__device__ __forceinline__ double sigmoid_key(float l) {
+  const double x = exp_within(double(fmaxf(-fabsf(l), -800.0f)));
+  return (l >= 0.0f ? 1.0 : x) * inverse(1.0 + x);
+}
 __device__ __forceinline__ double sigmoid(double l) {
-  const double x = exp(-fabs(l));
-  return (l >= 0.0 ? 1.0 : x) / (1.0 + x);
+  const double x = exp_down(-fabs(l));
+  return (l >= 0.0 ? 1.0 : x) * inverse(1.0 + x);
 }
 __device__ __forceinline__ double sigmoid_slope(double l) {
-  const double x = exp(-fabs(l));
-  return x / ((1.0 + x) * (1.0 + x));
+  const double x = exp_down(-fabs(l)), r = inverse(1.0 + x);
+  return x * r * r;
 }
 
 // ---------------------------------------------------------------------------
-// Lane r of a group's `width` lanes holds the group's experts r, r + width, ...
-// (one group: all lanes).
+// Lane r of a group's `width` lanes (one group: all lanes) holds the group's
+// experts r, r + width, ..., or, where the group's size is a multiple of four and
+// the logits and the bias are 16-byte aligned, r-th fours of neighbours: 16 loads
+// of two neighbouring floats a group became 4 loads (16384 tokens, 256 experts in
+// 8 groups: 22 -> 16 us).
 // ---------------------------------------------------------------------------
 template <int LANES, int PER, int KP>
-__global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width,
+__global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width, bool fours,
                                                          int64_t block0) {
   constexpr int kTokens = kBlock / LANES;
   const int li = int(threadIdx.x) & (LANES - 1);
@@ -174,14 +250,35 @@ __global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width,
   const bool live = t < a.T && (!a.token_count || t < a.token_count[0]);
   const int size = a.E / a.groups;
   const int g = li / width, first = li & (width - 1);
-  const float* row = a.logits + t * a.E;
-  float l[PER];
+  // every place is loaded, so that the loads go out together; what is none of
+  // the token's (a token past the end loads the last one's) becomes -infinity
+  const float* row = a.logits + (t < a.T ? t : a.T - 1) * a.E;
+  // place of the lane's j-th expert in its group: fours have steps of 1 inside
+  const int base = g * size + (fours ? 4 * first : first), inside = fours ? 1 : width;
+  auto expert = [&](int j) { return base + (j & 3) * inside + (j >> 2) * 4 * width; };
+  // experts from here on are none of the lane's
+  const int limit = g < a.groups ? (g + 1) * size : 0;
+  auto load = [&](const float* from, float (&v)[PER]) {
+    if (fours) {
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int i = j * width + first;
-    l[j] = -INFINITY;
-    if (live && g < a.groups && i < size) l[j] = row[g * size + i];
-  }
+      for (int j = 0; j < PER; j += 4) {
+        const int e = expert(j);
+        const float4 f = *reinterpret_cast<const float4*>(from + (e < a.E ? e : 0));
+        v[j] = f.x;
+        if (j + 1 < PER) v[j + 1] = f.y;
+        if (j + 2 < PER) v[j + 2] = f.z;
+        if (j + 3 < PER) v[j + 3] = f.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) v[j] = from[expert(j) < a.E ? expert(j) : 0];
+    }
+  };
+  float l[PER];
+  load(row, l);
+  const int own = live ? limit : 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) l[j] = expert(j) < own ? l[j] : -INFINITY;
   const bool by_score = a.bias || (a.groups > 1 && a.group_top == 2);
   const bool whole = !a.sigmoid && (by_score || !a.renorm);
   double most = 0.0, total = 1.0;
@@ -198,8 +295,8 @@ __global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width,
   if (whole) {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const double p = exp(k[j] - most);
-      total += g < a.groups && j * width + first < size ? p : 0.0;
+      const double p = exp_down(k[j] - most);
+      total += expert(j) < limit ? p : 0.0;
       if (by_score) k[j] = p;
     }
     total = over_lanes<LANES>(total, add);
@@ -210,19 +307,18 @@ __global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width,
     }
   } else if (by_score) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) k[j] = sigmoid(k[j]);
+    for (int j = 0; j < PER; ++j) k[j] = sigmoid_key(l[j]);
   }
   if (a.bias) {
+    float b[PER];
+    load(a.bias, b);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = j * width + first;
-      if (g < a.groups && i < size) k[j] += double(a.bias[g * size + i]);
-    }
+    for (int j = 0; j < PER; ++j) k[j] += double(b[j]);
   }
 #pragma unroll
   for (int j = 0; j < PER; ++j)
-    // false for a NaN on either side
-    if (!(l[j] > -INFINITY && k[j] > -INFINITY)) k[j] = kNone;
+    // a NaN on either side and -infinity: none
+    k[j] = fmax(l[j] > -INFINITY ? k[j] : kNone, kNone);
   if (a.groups > 1) {
     double b0 = kNone, b1 = kNone;
 #pragma unroll
@@ -230,25 +326,17 @@ __global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width,
       b1 = fmax(b1, fmin(b0, k[j]));
       b0 = fmax(b0, k[j]);
     }
-    for (int o = 1; o < width; o <<= 1) {
-      const double c0 = __shfl_xor(b0, o), c1 = __shfl_xor(b1, o);
-      b1 = fmax(fmin(b0, c0), fmax(b1, c1));
-      b0 = fmax(b0, c0);
-    }
+    best_two<LANES>(b0, b1, width);
     double worth = b0;
-    if (a.group_top == 2 && b1 > kNone) worth = b0 + b1;
-    if (b0 > kNone) worth = key_of(worth, g);
-    int before = 0;
-    for (int h = 0; h < a.groups; ++h)
-      before += from_lane(worth, (lane_id() & ~(LANES - 1)) + h * width) > worth ? 1 : 0;
-    if (before >= a.kept) {
+    if (a.group_top == 2 && b1 > kLowest) worth = b0 + b1;
+    if (b0 > kLowest) worth = key_of(worth, g);
+    if (better_lanes<LANES>(worth) >= a.kept * width) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) k[j] = kNone;
     }
   }
 #pragma unroll
-  for (int j = 0; j < PER; ++j)
-    if (k[j] > kNone) k[j] = key_of(k[j], g * size + j * width + first);
+  for (int j = 0; j < PER; ++j) k[j] = key_of(k[j], expert(j));
   double top[KP];
   {
     const Local<KP, PER> mine(k);
@@ -259,7 +347,7 @@ __global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width,
 #pragma unroll
   for (int i = 0; i < KP; ++i)
     if (li == i) mine = top[i];
-  const bool chosen = li < a.K && mine > kNone;
+  const bool chosen = li < a.K && mine > kLowest;
   const int e = chosen ? expert_of(mine) : -1;
   double s = 0.0;
   if (a.sigmoid) {
@@ -267,7 +355,7 @@ __global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width,
   } else {
     const float le = chosen ? row[e] : -INFINITY;
     if (a.renorm) most = over_lanes<16>(double(le), larger);
-    if (chosen) s = exp(double(le) - most);
+    if (chosen) s = exp_down(double(le) - most);
   }
   if (a.renorm) total = over_lanes<16>(s, add);
   if (t >= a.T || li >= a.K) return;
@@ -292,7 +380,7 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(RouteArgs a, int
   double* g = grad[int(threadIdx.x) / LANES];
 #pragma unroll
   for (int j = 0; j < PER; ++j) g[j * LANES + li] = 0.0;
-  const float* row = a.logits + t * a.E;
+  const float* row = a.logits + (live ? t : a.T - 1) * a.E;
   int e = -1;
   double d = 0.0;
   if (live && li < a.K) {
@@ -312,15 +400,18 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(RouteArgs a, int
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int i = j * LANES + li;
-      const float l = live && i < a.E ? row[i] : -INFINITY;
-      p[j] = double(l);
-      m = fmaxf(m, l);
+      p[j] = double(row[i < a.E ? i : 0]);
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (j * LANES + li >= a.E) p[j] = -INFINITY;
+      m = fmaxf(m, float(p[j]));
     }
     most = over_lanes<LANES>(double(m), larger);
     total = 0.0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      p[j] = exp(p[j] - most);
+      p[j] = exp_down(p[j] - most);
       if (j * LANES + li < a.E) total += p[j];
     }
     total = over_lanes<LANES>(total, add);
@@ -328,7 +419,7 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(RouteArgs a, int
     most = over_lanes<16>(double(le), larger);
   }
   if (e >= 0)
-    s = a.sigmoid ? sigmoid(double(le)) : le == -INFINITY ? 0.0 : exp(double(le) - most);
+    s = a.sigmoid ? sigmoid(double(le)) : le == -INFINITY ? 0.0 : exp_down(double(le) - most);
   if (a.renorm) total = over_lanes<16>(s, add);
   const double each = total != 0.0 ? 1.0 / total : 0.0;
   if (a.renorm || whole) {
@@ -370,8 +461,11 @@ template <int LANES, int PER, int KP>
 void launch_route_k(const RouteArgs& a, hipStream_t s) {
   const int64_t blocks = (a.T + kBlock / LANES - 1) / (kBlock / LANES);
   const int width = LANES / ceil_pow2(a.groups);
+  const bool fours = PER >= 4 && a.E / a.groups % 4 == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0;
   for_each_launch(blocks, kBlock, [&](int64_t b0, unsigned g) {
-    route_kernel<LANES, PER, KP><<<g, kBlock, 0, s>>>(a, width, b0);
+    route_kernel<LANES, PER, KP><<<g, kBlock, 0, s>>>(a, width, fours, b0);
   });
 }
 
