@@ -57,14 +57,52 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
+// That of the wide form, 2 M products a half: M LDS reads and M / 2 loads of weights in
+// the first, then LA writes; M reads in the second, then LA loads of rows.
+template <int M, int LA>
+__device__ __forceinline__ void interleave_wide() {
+  constexpr int kProduct = 0x008, kLoad = 0x020, kRead = 0x100, kWrite = 0x200;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kProduct, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+      if (h == 0 && i % 2 == 0) __builtin_amdgcn_sched_group_barrier(kLoad, 1, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kProduct, M / LA, 0);
+      if (h == 0) __builtin_amdgcn_sched_group_barrier(kWrite, 1, 0);
+      if (h == 1) __builtin_amdgcn_sched_group_barrier(kLoad, 1, 0);
+    }
+  }
+}
+
 struct LogitsGemm {
   const void* x;                 // [T][H] bf16
   const void* w;                 // [E][H] bf16
   int64_t T;
   int E, H;
-  int each;                      // stages of 64 channels a workgroup takes
+  int each;                      // stages a workgroup takes
   float* out;                    // [splits][T][E]
 };
+
+// 4 N neighbouring logits, of which `left` lie before the row's end.
+template <int N>
+__device__ __forceinline__ void store_neighbours(float* to, const f32x4 (&v)[N], int left, int E) {
+  if ((E & 3) == 0) {
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+      if (4 * t < left) __builtin_memcpy(to + 4 * t, &v[t], 16);
+  } else {
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * t + i < left) to[4 * t + i] = v[t][i];
+  }
+}
 
 // ---------------------------------------------------------------------------
 // out[t, e] = sum over h of x[t, h] w[e, h].  A workgroup takes 16 MT WM tokens
@@ -183,20 +221,135 @@ __global__ __launch_bounds__(kBlock) void logits_kernel(LogitsGemm g, int64_t mb
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = (wm * MT + m) * 16 + n;
-    if (row >= rows || col >= cols) continue;
-    float* to = out + int64_t(row) * g.E + col;
-    if ((g.E & 3) == 0) {
+    if (row < rows) store_neighbours<4>(out + int64_t(row) * g.E + col, acc[m], cols - col, g.E);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The same for many tokens: a workgroup takes 128 of them and 128 experts, a wave all
+// the tokens and 32 experts.  The weights come in the order of the matrix cores
+// (wf_kernel), straight into registers, 1 KB a load, so that LDS moves the tokens'
+// rows alone and a weight is loaded once for 128 tokens.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(kBlock, 2) void logits_wide_kernel(LogitsGemm g, const u32x4* wf,
+                                                                int nb, int64_t b0) {
+  constexpr int MT = kWideTokens / 16, kA = kWideTokens * 8, LA = kA / kBlock;
+  __shared__ u32x4 lds[3 * kA];
+  const int lane = lane_id(), n = lane & 15, q = lane >> 4;
+  // Workgroups go to the eight XCDs in turn: those of the same tokens are eight
+  // apart, so that the second finds the rows in its XCD's L2.
+  const int64_t b = b0 + blockIdx.x, turn = b / (8 * nb);
+  const int r = int(b - turn * (8 * nb));
+  const int64_t m0 = (turn * 8 + (r & 7)) * kWideTokens;
+  const int n0 = (r >> 3) * kWideExperts + wave_id() * 32;
+  if (m0 >= g.T) return;
+  const int rows = int(g.T - m0 < kWideTokens ? g.T - m0 : kWideTokens);
+  const int pitch = 2 * g.H;                             // bytes of a row
+  const rsrc_t ar = make_rsrc(static_cast<const uint16_t*>(g.x) + m0 * g.H, int64_t(rows) * pitch);
+  const int stages = (g.H + 63) / 64;
+  const int st0 = int(blockIdx.z) * g.each;
+  const int count = stages - st0 < g.each ? stages - st0 : g.each;
+  const int row0 = int(threadIdx.x) >> 3, piece = int(threadIdx.x) & 7;
+  const uint32_t off0 = uint32_t(row0) * uint32_t(pitch) + uint32_t(piece * 16);
+  const uint32_t step = 32u * uint32_t(pitch);
+  const bool own = n0 < g.E;                             // else the wave has no experts
+  const u32x4* w = wf + int64_t(own ? n0 >> 5 : 0) * stages * (4 * kWave) + lane;
+  u32x4 av[3][LA], wv[3][2][2];
+  auto load_x = [&](int d, int i0) {
+    const int st = st0 + i0;
+    const bool in = i0 < count && st * 64 + piece * 8 < g.H;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (col + 4 * t < cols) __builtin_memcpy(to + 4 * t, &acc[m][t], 16);
-    } else {
+    for (int i = 0; i < LA; ++i)
+      av[d][i] = __builtin_amdgcn_raw_buffer_load_b128(
+          ar, (in ? off0 : kOob) + uint32_t(i) * step, i0 < count ? st * 128 : 0, 0);
+  };
+  auto load_w = [&](int d, int i0) {
+    // past the end the last stage's weights meet rows of zeros
+    const u32x4* from = w + int64_t(st0 + (i0 < count ? i0 : count - 1)) * (4 * kWave);
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (col + 4 * t + i < cols) to[4 * t + i] = acc[m][t][i];
+      for (int t = 0; t < 2; ++t) wv[d][s][t] = from[(s * 2 + t) * kWave];
+  };
+  auto write = [&](int d, int buf) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i)
+      lds[buf * kA + (row0 + i * 32) * 8 + (piece ^ (row0 & 7))] = av[d][i];
+  };
+  auto read = [&](int buf, int s, u32x4 (&a)[MT]) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      a[m] = lds[buf * kA + (m * 16 + n) * 8 + ((s * 4 + q) ^ (n & 7))];
+  };
+  f32x4 acc[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 a0[MT], a1[MT];
+  auto products = [&](const u32x4 (&a)[MT], const u32x4 (&b)[2]) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) acc[m][t] = mfma(b[t], a[m], acc[m][t]);
+  };
+  // issued in the loop's order, for the waits at its top count the loads after
+  // the one they wait for on both ways there
+  load_x(0, 0);
+  load_x(1, 1);
+  load_x(2, 2);
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(0, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  write(0, 0);
+  load_x(0, 3);
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(1, 1);
+  __builtin_amdgcn_sched_barrier(0);
+  write(1, 1);
+  load_x(1, 4);
+  __builtin_amdgcn_sched_barrier(0);
+  lds_barrier();
+  read(0, 0, a0);
+  for (int st = 0; st < count; st += 3) {
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+      // as in logits_kernel; the weights are two stages ahead: loads return in
+      // order, so that a wait for them is one for the rows loaded before them
+      load_w((d + 2) % 3, st + d + 2);
+      read(d, 1, a1);
+      products(a0, wv[d][0]);
+      write((d + 2) % 3, (d + 2) % 3);
+      load_x((d + 2) % 3, st + d + 5);
+      read((d + 1) % 3, 0, a0);
+      products(a1, wv[d][1]);
+      interleave_wide<MT, LA>();
+      lds_barrier();
     }
   }
+  if (!own) return;
+  float* out = g.out + (int64_t(blockIdx.z) * g.T + m0) * g.E + n0;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int row = m * 16 + n;
+    if (row < rows)
+      store_neighbours<2>(out + int64_t(row) * g.E + q * 8, acc[m], g.E - n0 - q * 8, g.E);
+  }
+}
+
+// wf: the weights in the matrix cores' order, [experts / 32][channels / 32][2 tiles]
+// blocks of 1 KB, 16 bytes a lane: lane (n, q) holds channels 8 q and on of the
+// block's 32 of row n, which stands for expert (n / 4) * 8 + tile * 4 + n % 4 of 32;
+// zeros past the ends.
+__global__ __launch_bounds__(kBlock) void wf_kernel(const u32x4* w, int E, int H, int Ep,
+                                                    int64_t Hp, u32x4* out) {
+  const int64_t at = int64_t(blockIdx.x) * kBlock + threadIdx.x;
+  const int H8 = int(Hp >> 3);
+  const int e = int(at / H8), h8 = int(at - int64_t(e) * H8);
+  if (e >= Ep) return;
+  const u32x4 v = e < E && h8 * 8 < H ? w[int64_t(e) * (H >> 3) + h8] : u32x4{0u, 0u, 0u, 0u};
+  const int r = (e & 3) | ((e >> 3) & 3) << 2, tile = (e >> 2) & 1;
+  out[((int64_t(e >> 5) * (H8 >> 2) + (h8 >> 2)) * 2 + tile) * kWave + (h8 & 3) * 16 + r] = v;
 }
 
 // A float as the sum of three bf16 numbers, exact where the last is no smaller
@@ -484,7 +637,20 @@ hipError_t launch_router_logits(const LogitsArgs& a, hipStream_t s) {
   g.H = a.H;
   g.each = shape.each;
   g.out = shape.splits > 1 ? static_cast<float*>(a.ws) : a.logits;
-  if (shape.bm == 16)
+  if (shape.wide) {
+    const WideSpace at = wide_space(shape, a.T, a.E, a.H);
+    char* ws = static_cast<char*>(a.ws);
+    u32x4* wf = reinterpret_cast<u32x4*>(ws + at.wf);
+    if (shape.splits > 1) g.out = reinterpret_cast<float*>(ws + at.part);
+    const int64_t pieces = at.experts * (at.channels >> 3);
+    wf_kernel<<<unsigned((pieces + kBlock - 1) / kBlock), kBlock, 0, s>>>(
+        static_cast<const u32x4*>(a.w), a.E, a.H, int(at.experts), at.channels, wf);
+    const int64_t blocks = (shape.mb + 7) / 8 * 8 * shape.nb;
+    for_each_launch(blocks, kBlock * shape.splits, [&](int64_t b0, unsigned n) {
+      const dim3 grid{n, 1u, unsigned(shape.splits)};
+      logits_wide_kernel<<<grid, kBlock, 0, s>>>(g, wf, shape.nb, b0);
+    });
+  } else if (shape.bm == 16)
     launch_logits_shape<1, 1, 4>(g, shape, s);
   else if (shape.bm == 32)
     launch_logits_shape<2, 1, 4>(g, shape, s);
@@ -495,7 +661,7 @@ hipError_t launch_router_logits(const LogitsArgs& a, hipStream_t s) {
   else
     launch_logits_shape<4, 1, 4>(g, shape, s);
   if (shape.splits > 1)
-    launch_sum_rows(static_cast<const float*>(a.ws), shape.splits, a.T * a.E, a.logits, s);
+    launch_sum_rows(g.out, shape.splits, a.T * a.E, a.logits, s);
   return hipGetLastError();
 }
 

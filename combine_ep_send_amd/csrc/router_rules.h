@@ -60,14 +60,20 @@ struct LogitsShape {
   int bm, wn;
   int64_t mb;
   int nb, splits, each;
+  bool wide;                     // the form with the weights in the matrix cores' order
 };
+
+constexpr int kWideTokens = 128, kWideExperts = 128;
 
 inline LogitsShape logits_shape(int64_t T, int E, int H) {
   LogitsShape g{};
-  g.bm = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  g.wn = E <= 64 ? 1 : E <= 128 ? 2 : 4;
+  g.wide = E > 128 && T >= 2048;
+  g.bm = g.wide ? kWideTokens : T <= 16 ? 16 : T <= 32 ? 32 : 64;
+  if (g.bm < 64) g.wn = 4;
+  const int experts = g.wide ? kWideExperts : 64 * g.wn;
   g.mb = T > 0 ? (T + g.bm - 1) / g.bm : 1;
-  g.wn = g.bm < 64 ? 4 : E <= 64 ? 1 : E <= 128 ? 2 : 4;
-  g.nb = (E + 64 * g.wn - 1) / (64 * g.wn);
+  g.nb = (E + experts - 1) / experts;
   const int stages = (H + 63) / 64;
   int64_t want = kGemmGroups / (g.mb * g.nb);
   if (want < 1) want = 1;
@@ -121,10 +127,27 @@ inline DwShape dw_shape(int64_t T, int E, int H) {
 }
 
 // Workspaces.
-inline int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
+constexpr int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 
+struct WideSpace {
+  int64_t experts;   // of the copy of the weights: whole waves
+  int64_t channels;  // whole stages
+  size_t wf;         // the weights in the matrix cores' order
+  size_t part;       // [splits][T][E] fp32
+  size_t total;
+};
+inline WideSpace wide_space(const LogitsShape& g, int64_t T, int E, int H) {
+  WideSpace s{};
+  s.experts = (E + 31) / 32 * 32;
+  s.channels = pad64(H);
+  s.wf = 0;
+  s.part = (size_t(s.experts) * size_t(s.channels) * 2 + 255) / 256 * 256;
+  s.total = s.part + (g.splits > 1 ? size_t(g.splits) * size_t(T) * size_t(E) * 4 : 0);
+  return s;
+}
 inline size_t logits_ws_bytes(int64_t T, int E, int H) {
   const LogitsShape g = logits_shape(T, E, H);
+  if (g.wide) return wide_space(g, T, E, H).total;
   return 256 + (g.splits > 1 ? size_t(g.splits) * size_t(T) * size_t(E) * 4 : 0);
 }
 
