@@ -14,7 +14,8 @@ using namespace epdc;
 
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 
-static_assert(kRouterChannels == EPDC_ROUTER_CHANNELS, "limits");
+static_assert(kRouterChannels == EPDC_ROUTER_CHANNELS && kNormChannels == EPDC_NORM_CHANNELS,
+              "limits");
 
 bool is_aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
@@ -25,15 +26,14 @@ bool array_ok(const void* p, int64_t count, uintptr_t a) {
 bool maybe_ok(const void* p, uintptr_t a) { return p == nullptr || is_aligned(p, a); }
 int launched(hipError_t e) { return e == hipSuccess ? EP_OK : EP_ERR_LAUNCH; }
 
-// Tokens and channels of the norm and of the router.
-int check_tokens(int64_t tokens, int hidden) {
+int check_tokens(int64_t tokens, int hidden, int most) {
   if (tokens < 0 || hidden <= 0 || hidden % 8 != 0) return EP_ERR_INVALID_ARG;
-  if (tokens >= kMaxRows || hidden > EPDC_ROUTER_CHANNELS) return EP_ERR_UNSUPPORTED;
+  if (tokens >= kMaxRows || hidden > most) return EP_ERR_UNSUPPORTED;
   return EP_OK;
 }
 
 int check_logits(int64_t tokens, int experts, int hidden) {
-  const int st = check_tokens(tokens, hidden);
+  const int st = check_tokens(tokens, hidden, EPDC_ROUTER_CHANNELS);
   if (st != EP_OK) return st;
   return experts < 1 ? EP_ERR_INVALID_ARG : experts > EPDC_MAX_BINS ? EP_ERR_UNSUPPORTED : EP_OK;
 }
@@ -55,7 +55,7 @@ int ep_router_abi_version(void) { return EPDC_ROUTER_ABI_VERSION; }
 int ep_rms_norm(const void* x, const void* residual, const void* weight, int weight_type,
                 int64_t num_tokens, int hidden, float eps, void* residual_out, void* out, void* q,
                 float* scale, int scale_fmt, float* rstd, hipStream_t stream) {
-  const int st = check_tokens(num_tokens, hidden);
+  const int st = check_tokens(num_tokens, hidden, EPDC_NORM_CHANNELS);
   if (st != EP_OK) return st;
   if (weight_type != EP_NORM_W_BF16 && weight_type != EP_NORM_W_F32) return EP_ERR_INVALID_ARG;
   if (scale_fmt != EP_SCALE_F32 && scale_fmt != EP_SCALE_POW2) return EP_ERR_INVALID_ARG;
@@ -85,16 +85,16 @@ int ep_rms_norm(const void* x, const void* residual, const void* weight, int wei
 }
 
 size_t ep_rms_norm_backward_workspace_bytes(int64_t num_tokens, int hidden) {
-  if (check_tokens(num_tokens, hidden) != EP_OK) return 0;
+  if (check_tokens(num_tokens, hidden, EPDC_NORM_CHANNELS) != EP_OK) return 0;
   // one row even for no tokens, so that 0 says refused
-  return size_t(num_tokens ? norm_groups(num_tokens) : 1) * size_t(hidden) * 4;
+  return size_t(num_tokens ? norm_groups(num_tokens, hidden) : 1) * size_t(hidden) * 4;
 }
 
 int ep_rms_norm_backward(const void* dy, const void* s, const void* weight, int weight_type,
                          const float* rstd, const void* d_residual, int64_t num_tokens, int hidden,
                          void* dx, float* dweight, void* workspace, size_t workspace_bytes,
                          hipStream_t stream) {
-  const int st = check_tokens(num_tokens, hidden);
+  const int st = check_tokens(num_tokens, hidden, EPDC_NORM_CHANNELS);
   if (st != EP_OK) return st;
   if (weight_type != EP_NORM_W_BF16 && weight_type != EP_NORM_W_F32) return EP_ERR_INVALID_ARG;
   if (!array_ok(weight, 1, 16)) return EP_ERR_INVALID_ARG;

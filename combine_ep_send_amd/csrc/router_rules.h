@@ -11,6 +11,9 @@ constexpr int kRouterChannels = 65536;
 
 // ---- norm -------------------------------------------------------------------
 // A workgroup takes a row at a time; a thread holds PT 16-byte pieces of it.
+constexpr int kNormChannels = 32768;
+constexpr int kNormMaxThreads = 512;
+
 struct NormShape {
   int pieces;      // PT: 1, 2, 4 or 8
   int threads;
@@ -19,14 +22,29 @@ struct NormShape {
 inline NormShape norm_shape(int H) {
   const int n = H / 8;
   int pt = 1;
-  while (pt < 8 && n > pt * 512) pt *= 2;
+  while (pt < 8 && n > pt * kNormMaxThreads) pt *= 2;
   const int t = (n + pt - 1) / pt;
   return NormShape{pt, (t + 63) / 64 * 64};
 }
 
 // Workgroups of the backward pass, each with one row of partial sums of the
-// weight's gradient.
-inline int norm_groups(int64_t T) { return int(T < 1024 ? T : 1024); }
+// weight's gradient: as many as the chip holds at once, by the waves that the
+// kernel's registers allow a compute unit.
+inline int norm_groups(int64_t T, int H) {
+  const NormShape n = norm_shape(H);
+  const int waves = n.pieces == 1 ? 24 : n.pieces == 2 ? 16 : 8;
+  int per_cu = waves / (n.threads / 64);
+  if (per_cu < 1) per_cu = 1;
+  if (per_cu > 4) per_cu = 4;
+  const int most = 256 * per_cu;
+  return int(T < most ? T : most);
+}
+
+// Whether rows are read with non-temporal loads: `inputs` arrays of rows that come
+// to one and a half times the Infinity Cache.
+inline bool norm_streams(int64_t T, int H, int inputs) {
+  return T * H * 2 * inputs >= int64_t(384) << 20;
+}
 
 // ---- choice of the experts ----------------------------------------------------
 // A token is chosen for by `lanes` lanes (16 or 64), each holding up to `per`

@@ -26,7 +26,8 @@ extern "C" {
 #endif
 
 #define EPDC_ROUTER_ABI_VERSION 1
-/* Channels of a row of the norm and of the router. */
+/* Channels of a row of the norm, and of the router. */
+#define EPDC_NORM_CHANNELS 32768
 #define EPDC_ROUTER_CHANNELS 65536
 /* Groups of experts ep_route chooses from. */
 #define EPDC_MAX_GROUPS 16
@@ -61,7 +62,7 @@ typedef enum { EP_NORM_W_BF16 = 0, EP_NORM_W_F32 = 1 } ep_norm_weight_t;
  *                 multiple of 128); scale [T,H/128] fp32 out, NULL with q
  *   scale_fmt     EP_SCALE_F32 or EP_SCALE_POW2
  *   rstd          [T] fp32 out, or NULL: ep_rms_norm_backward takes it
- * H is a multiple of 8, <= EPDC_ROUTER_CHANNELS.  One of out and q is given.
+ * H is a multiple of 8, <= EPDC_NORM_CHANNELS.  One of out and q is given.
  */
 int ep_rms_norm(const void* x, const void* residual, const void* weight, int weight_type,
                 int64_t num_tokens, int hidden, float eps, void* residual_out, void* out, void* q,

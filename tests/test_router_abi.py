@@ -38,7 +38,7 @@ def test_norm_refusals():
                 s=None, fmt=0, rstd=None, st=None)
     refusals(_lib.lib().ep_rms_norm, args, [
         (dict(T=-1), BAD), (dict(T=1 << 30), UNS), (dict(H=0), BAD), (dict(H=-8), BAD),
-        (dict(H=12), BAD), (dict(H=65544), UNS), (dict(wt=2), BAD), (dict(wt=-1), BAD),
+        (dict(H=12), BAD), (dict(H=32776), UNS), (dict(wt=2), BAD), (dict(wt=-1), BAD),
         (dict(eps=-1e-6), BAD), (dict(eps=float("nan")), BAD), (dict(eps=float("inf")), BAD),
         (dict(fmt=2), BAD), (dict(fmt=-1), BAD), (dict(x=None), BAD), (dict(x=ODD16), BAD),
         (dict(w=None), BAD), (dict(w=ODD16), BAD), (dict(res=A16), BAD), (dict(ro=A16), BAD),
@@ -56,7 +56,7 @@ def test_norm_backward_refusals():
                 bytes=1 << 20, st=None)
     refusals(L.ep_rms_norm_backward, args, [
         (dict(T=-1), BAD), (dict(T=1 << 30), UNS), (dict(H=0), BAD), (dict(H=12), BAD),
-        (dict(H=1 << 17), UNS), (dict(wt=2), BAD), (dict(dy=None), BAD), (dict(dy=ODD16), BAD),
+        (dict(H=1 << 16), UNS), (dict(wt=2), BAD), (dict(dy=None), BAD), (dict(dy=ODD16), BAD),
         (dict(s=None), BAD), (dict(s=ODD16), BAD), (dict(w=None), BAD), (dict(rstd=None), BAD),
         (dict(rstd=ODD4), BAD), (dict(dr=ODD16), BAD), (dict(dx=None), BAD), (dict(dx=ODD16), BAD),
         (dict(dw=ODD4), BAD), (dict(ws=None), WS), (dict(ws=A16), WS),
@@ -64,7 +64,7 @@ def test_norm_backward_refusals():
         (dict(T=0, dy=None, s=None, rstd=None, dx=None, dw=None, ws=None, bytes=0), 0)])
     assert size(2, 256) == 2 * 256 * 4
     assert size(0, 256) > 0
-    for bad in ((-1, 256), (1 << 30, 256), (2, 0), (2, 12), (2, 65544), ((1 << 63) - 1, 256)):
+    for bad in ((-1, 256), (1 << 30, 256), (2, 0), (2, 12), (2, 32776), ((1 << 63) - 1, 256)):
         assert size(*bad) == 0
 
 
