@@ -10,7 +10,8 @@ namespace {
 constexpr int kNormMaxWaves = kNormMaxThreads / kWave;
 constexpr int64_t kNormMaxGrid = 1 << 20;       // rows past it come round again
 
-__device__ __forceinline__ float wave_sum(float v) {
+template <typename F>
+__device__ __forceinline__ F wave_sum(F v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
@@ -19,13 +20,14 @@ __device__ __forceinline__ float wave_sum(float v) {
 // Sum over the workgroup, the same in every thread: lanes first, then waves in
 // order.  `part` alternates between two rows from one call to the next, so that
 // one barrier a call is enough.
-__device__ __forceinline__ float block_sum(float v, float* part) {
+template <typename F>
+__device__ __forceinline__ F block_sum(F v, F* part) {
   v = wave_sum(v);
   const int waves = int(blockDim.x) / kWave;
   if (waves == 1) return v;
   if (lane_id() == 0) part[wave_id()] = v;
   __syncthreads();
-  float s = 0.0f;
+  F s = 0;
   for (int w = 0; w < waves; ++w) s += part[w];
   return s;
 }
@@ -58,13 +60,15 @@ __device__ __forceinline__ void load_weight(const void* weight, int j, float (&w
   }
 }
 
-// e4m3 codes and scale of 128 fp32 values held by 16 lanes, 8 each: the rules
-// of the dispatch's fp8 rows.  NaN is left out of amax; only a lane with one, or
+// e4m3 codes and scale of 128 values held by 16 lanes, 8 each, in 64 bits (v) and
+// rounded to fp32 (y): the rules of the dispatch's fp8 rows, the quotient rounded
+// once.  v / scale is v times 1 / scale in 64 bits, one division for the lane.  NaN is left out of amax; only a lane with one, or
 // a group with an infinity, needs the encoder that knows NaN.  A quotient passes
 // 448 by 2^-23 of it, or by more where the scale is subnormal; past 464 the
 // conversion instruction gives NaN, so the quotients are clamped first, which
 // is the saturation the codes call for.
-__device__ __forceinline__ u32x2 quantize_group(const float (&y)[8], bool pow2, float& scale) {
+__device__ __forceinline__ u32x2 quantize_group(const double (&v)[8], const float (&y)[8],
+                                                bool pow2, float& scale) {
   uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
@@ -83,14 +87,16 @@ __device__ __forceinline__ u32x2 quantize_group(const float (&y)[8], bool pow2, 
   if (pow2) scale = pow2_ceil(scale);
   if (!lane_nan && m != 0x7F800000u) {
     if (scale == 0.0f) return u32x2{0u, 0u};
-    float v[8];
+    const double inverse = 1.0 / double(scale);
+    float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_fmed3f(y[i] / scale, -448.0f, 448.0f);
+    for (int i = 0; i < 8; ++i)
+      t[i] = __builtin_amdgcn_fmed3f(float(v[i] * inverse), -448.0f, 448.0f);
     u32x2 c;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j], v[4 * j + 1], 0, false);
-      c[j] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j + 2], v[4 * j + 3], w, true));
+      const int w = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * j], t[4 * j + 1], 0, false);
+      c[j] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * j + 2], t[4 * j + 3], w, true));
     }
     return c;
   }
@@ -104,13 +110,17 @@ __device__ __forceinline__ u32x2 quantize_group(const float (&y)[8], bool pow2, 
 
 // ---------------------------------------------------------------------------
 // Forward: one workgroup a row, the row in registers between the sum of squares
-// and the output, so that every byte moves once.  A thread's pieces lie a
+// and the output, so that every byte moves once.  The squares of eight neighbours
+// add up in fp32, the rest of the row's sum in 64 bits, and so are the values that
+// become codes (Q): the codes are then the roundings of the formula's values but for
+// about one in 10^7, instead of one in 10^5, at the same speed (a value that goes to
+// bf16 alone is in fp32).  A thread's pieces lie a
 // workgroup apart: consecutive threads move consecutive 16-byte pieces, and 16
 // neighbours hold a 128-channel group.
 // ---------------------------------------------------------------------------
-template <int PT, bool W32, bool NT>
+template <int PT, bool W32, bool NT, bool Q>
 __global__ __launch_bounds__(kNormMaxThreads) void rms_norm_kernel(NormArgs a) {
-  __shared__ float part[2][kNormMaxWaves];
+  __shared__ double part[2][kNormMaxWaves];
   const int H8 = a.H >> 3, n = int(blockDim.x);
   int turn = 0;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
@@ -143,16 +153,18 @@ __global__ __launch_bounds__(kNormMaxThreads) void rms_norm_kernel(NormArgs a) {
         if (j < H8) st_stream(ro + j, v[i]);
       }
     }
-    float sum = 0.0f;
+    double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
-      float f[8];
+      float f[8], s = 0.0f;
       unpack8(v[i], f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = __builtin_fmaf(f[k], f[k], sum);
+      for (int k = 0; k < 8; ++k) s = __builtin_fmaf(f[k], f[k], s);
+      sum += double(s);
     }
-    const float rstd = 1.0f / sqrtf(block_sum(sum, part[turn]) / float(a.H) + a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[t] = rstd;
+    const double rstd =
+        1.0 / sqrt(block_sum(sum, part[turn]) / double(a.H) + double(a.eps));
+    if (a.rstd && threadIdx.x == 0) a.rstd[t] = float(rstd);
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
       const int j = i * n + int(threadIdx.x);
@@ -160,12 +172,20 @@ __global__ __launch_bounds__(kNormMaxThreads) void rms_norm_kernel(NormArgs a) {
       float f[8], w[8];
       unpack8(v[i], f);
       load_weight<W32>(a.weight, j, w);
+      double y[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = f[k] * rstd * w[k];
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (Q) {
+          y[k] = double(f[k]) * rstd * double(w[k]);
+          f[k] = float(y[k]);
+        } else {
+          f[k] = f[k] * float(rstd) * w[k];
+        }
+      }
       if (a.out) st_stream(static_cast<u32x4*>(a.out) + t * H8 + j, pack8(f));
-      if (a.q) {
+      if constexpr (Q) {
         float scale;
-        static_cast<u32x2*>(a.q)[t * H8 + j] = quantize_group(f, a.pow2, scale);
+        static_cast<u32x2*>(a.q)[t * H8 + j] = quantize_group(y, f, a.pow2, scale);
         if ((j & 15) == 0) a.scale[t * (H8 >> 4) + (j >> 4)] = scale;
       }
     }
@@ -274,10 +294,14 @@ void launch_norm_pt(const NormArgs& a, bool backward, unsigned g, int threads, h
     rms_norm_backward_kernel<PT, W32, true><<<g, threads, 0, s>>>(a);
   else if (backward)
     rms_norm_backward_kernel<PT, W32, false><<<g, threads, 0, s>>>(a);
+  else if (a.q && nt)
+    rms_norm_kernel<PT, W32, true, true><<<g, threads, 0, s>>>(a);
+  else if (a.q)
+    rms_norm_kernel<PT, W32, false, true><<<g, threads, 0, s>>>(a);
   else if (nt)
-    rms_norm_kernel<PT, W32, true><<<g, threads, 0, s>>>(a);
+    rms_norm_kernel<PT, W32, true, false><<<g, threads, 0, s>>>(a);
   else
-    rms_norm_kernel<PT, W32, false><<<g, threads, 0, s>>>(a);
+    rms_norm_kernel<PT, W32, false, false><<<g, threads, 0, s>>>(a);
 }
 
 template <bool W32>

@@ -41,12 +41,15 @@ typedef enum { EP_NORM_W_BF16 = 0, EP_NORM_W_F32 = 1 } ep_norm_weight_t;
 /*
  * RMS norm, after the residual's addition where there is one:
  *   s[t,:]  = bf16( x[t,:] + residual[t,:] )        (fp32 sum; s = x without)
- *   rstd[t] = 1 / sqrt( mean(s[t,:]^2) + eps )      (fp32)
- *   y[t,h]  = s[t,h] * rstd[t] * weight[h]          (fp32)
- *   out     = bf16(y)
- *   q, scale: e4m3 codes and one scale per 128 channels of y, quantized from
- *             fp32: amax = max |y|, scale = fp32(amax / 448), or the smallest
- *             power of two at or above that, code = e4m3(fp32(y / scale)).
+ *   rstd[t] = 1 / sqrt( mean(s[t,:]^2) + eps )
+ *   y[t,h]  = s[t,h] * rstd[t] * weight[h]
+ *   out     = bf16(fp32(y))
+ *   q, scale: e4m3 codes and one scale per 128 channels of y, not of out: amax =
+ *             max |fp32(y)|, scale = fp32(amax / 448), or the smallest power of
+ *             two at or above that, code = e4m3(fp32(y / scale)).
+ * rstd is in 64 bits, from fp32 sums of the squares of eight neighbours (a sum past
+ * fp32, channels of 2^62 and more, makes it 0); y is in 64 bits where there are
+ * codes, in fp32 without.
  * The rounding of the codes, saturation, zeros, NaN and infinities follow
  * ep_dispatch_permute's fp8 form.  A group whose scale is 0 (amax below
  * 448 * 2^-150) has codes 0.

@@ -123,7 +123,8 @@ def test_in_place_and_given_outputs():
     over = ep.ep_rms_norm(x2, w, residual=r, residual_out=x2)
     for a, b in ((got.residual, want.residual), (got.y, want.y), (got.scale, want.scale),
                  (got.rstd, want.rstd), (got.q.view(torch.uint8), want.q.view(torch.uint8)),
-                 (over.residual, want.residual), (over.y, want.y)):
+                 (over.residual, want.residual),
+                 (over.y, ep.ep_rms_norm(x, w, residual=r).y)):
         assert torch.equal(a, b)
 
 
