@@ -88,19 +88,20 @@ struct LogitsGemm {
   float* out;                    // [splits][T][E]
 };
 
-// 4 N neighbouring logits, of which `left` lie before the row's end.
+// A lane's logits of N tiles, four neighbours every 16; `left` experts lie before the
+// row's end.
 template <int N>
-__device__ __forceinline__ void store_neighbours(float* to, const f32x4 (&v)[N], int left, int E) {
+__device__ __forceinline__ void store_tiles(float* to, const f32x4 (&v)[N], int left, int E) {
   if ((E & 3) == 0) {
 #pragma unroll
     for (int t = 0; t < N; ++t)
-      if (4 * t < left) __builtin_memcpy(to + 4 * t, &v[t], 16);
+      if (16 * t < left) __builtin_memcpy(to + 16 * t, &v[t], 16);
   } else {
 #pragma unroll
     for (int t = 0; t < N; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (4 * t + i < left) to[4 * t + i] = v[t][i];
+        if (16 * t + i < left) to[16 * t + i] = v[t][i];
   }
 }
 
@@ -118,9 +119,8 @@ __device__ __forceinline__ void store_neighbours(float* to, const f32x4 (&v)[N],
 // channels past the end.
 // LDS holds a row of a stage as eight 16-byte pieces, permuted by three bits of
 // the row, so that the eight rows that a read takes at once lie in different
-// banks.  w is the instruction's first operand, so that a lane's four results
-// are neighbouring experts, and row r of tile i is row (r / 4) * 16 + i * 4 + r % 4
-// of the wave's 64, so that its four tiles are too.
+// banks.  w is the instruction's first operand, so that a lane's four results are
+// neighbouring experts.
 // ---------------------------------------------------------------------------
 template <int MT, int WM, int WN>
 __global__ __launch_bounds__(kBlock) void logits_kernel(LogitsGemm g, int64_t mb0) {
@@ -145,9 +145,7 @@ __global__ __launch_bounds__(kBlock) void logits_kernel(LogitsGemm g, int64_t mb
   const int row0 = int(threadIdx.x) >> 3, piece = int(threadIdx.x) & 7;
   const uint32_t off0 = uint32_t(row0) * uint32_t(pitch) + uint32_t(piece * 16);
   const uint32_t step = 32u * uint32_t(pitch);
-  // rows: piece p of row r lies at p ^ a(r), p ^ b(r)
-  const int awrite = row0 * 8 + (piece ^ (row0 & 7));
-  const int bwrite = kA + row0 * 8 + (piece ^ ((row0 & 3) | ((row0 >> 2) & 4)));
+  const int awrite = row0 * 8 + (piece ^ (row0 & 7)), bwrite = kA + awrite;
   u32x4 av[R][LA], bv[R][LB];
   auto load = [&](int d, int i0) {
     const int st = st0 + i0;
@@ -169,15 +167,14 @@ __global__ __launch_bounds__(kBlock) void logits_kernel(LogitsGemm g, int64_t mb
 #pragma unroll
     for (int i = 0; i < LB; ++i) to[bwrite + i * 256] = bv[d][i];
   };
-  const int aread = (wm * 16 * MT + n) * 8, bread = kA + (wn * 64 + (n >> 2) * 16 + (n & 3)) * 8;
+  const int aread = (wm * 16 * MT + n) * 8, bread = kA + (wn * 64 + n) * 8;
   auto read = [&](int buf, int s, u32x4 (&a)[MT], u32x4 (&b)[4]) {
     const u32x4* from = lds + buf * (kA + kB);
-    const int at = s * 4 + q;
+    const int at = (s * 4 + q) ^ (n & 7);
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      b[t] = from[bread + t * 32 + (at ^ ((n & 3) | (n & 4)))];
+    for (int t = 0; t < 4; ++t) b[t] = from[bread + t * 128 + at];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) a[m] = from[aread + m * 128 + (at ^ (n & 7))];
+    for (int m = 0; m < MT; ++m) a[m] = from[aread + m * 128 + at];
   };
   f32x4 acc[MT][4];
 #pragma unroll
@@ -217,11 +214,11 @@ __global__ __launch_bounds__(kBlock) void logits_kernel(LogitsGemm g, int64_t mb
     }
   }
   float* out = g.out + (int64_t(blockIdx.z) * g.T + m0) * g.E + n0;
-  const int col = wn * 64 + q * 16;
+  const int col = wn * 64 + q * 4;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = (wm * MT + m) * 16 + n;
-    if (row < rows) store_neighbours<4>(out + int64_t(row) * g.E + col, acc[m], cols - col, g.E);
+    if (row < rows) store_tiles<4>(out + int64_t(row) * g.E + col, acc[m], cols - col, g.E);
   }
 }
 
@@ -333,14 +330,13 @@ __global__ __launch_bounds__(kBlock, 2) void logits_wide_kernel(LogitsGemm g, co
   for (int m = 0; m < MT; ++m) {
     const int row = m * 16 + n;
     if (row < rows)
-      store_neighbours<2>(out + int64_t(row) * g.E + q * 8, acc[m], g.E - n0 - q * 8, g.E);
+      store_tiles<2>(out + int64_t(row) * g.E + q * 4, acc[m], g.E - n0 - q * 4, g.E);
   }
 }
 
 // wf: the weights in the matrix cores' order, [experts / 32][channels / 32][2 tiles]
 // blocks of 1 KB, 16 bytes a lane: lane (n, q) holds channels 8 q and on of the
-// block's 32 of row n, which stands for expert (n / 4) * 8 + tile * 4 + n % 4 of 32;
-// zeros past the ends.
+// block's 32 of expert n of the tile; zeros past the ends.
 __global__ __launch_bounds__(kBlock) void wf_kernel(const u32x4* w, int E, int H, int Ep,
                                                     int64_t Hp, u32x4* out) {
   const int64_t at = int64_t(blockIdx.x) * kBlock + threadIdx.x;
@@ -348,8 +344,8 @@ __global__ __launch_bounds__(kBlock) void wf_kernel(const u32x4* w, int E, int H
   const int e = int(at / H8), h8 = int(at - int64_t(e) * H8);
   if (e >= Ep) return;
   const u32x4 v = e < E && h8 * 8 < H ? w[int64_t(e) * (H >> 3) + h8] : u32x4{0u, 0u, 0u, 0u};
-  const int r = (e & 3) | ((e >> 3) & 3) << 2, tile = (e >> 2) & 1;
-  out[((int64_t(e >> 5) * (H8 >> 2) + (h8 >> 2)) * 2 + tile) * kWave + (h8 & 3) * 16 + r] = v;
+  out[((int64_t(e >> 5) * (H8 >> 2) + (h8 >> 2)) * 2 + ((e >> 4) & 1)) * kWave +
+      (h8 & 3) * 16 + (e & 15)] = v;
 }
 
 // A float as the sum of three bf16 numbers, exact where the last is no smaller
@@ -368,16 +364,14 @@ __device__ __forceinline__ uint32_t half(uint32_t lo, uint32_t hi) { return lo |
 // Operands of the gradients' products in the order in which the matrix cores
 // take them: blocks of 1 KB, 16 bytes a lane, lane (n, q) = (lane & 15, lane >> 4)
 // holding eight k of row n, k = 8 q and on of the block's 32.  A wave then loads
-// a block as one run of memory.  Row r of tile i stands for row
-// (r / 4) * 16 + i * 4 + r % 4 of 64 (wt), or i * 16 + r (columns).
+// a block as one run of memory.
 // ---------------------------------------------------------------------------
 
 // columns: dlogits transposed, [Ep / 64][Tp / 32][4 tiles][3 parts] blocks: rows
 // are experts, k tokens; zeros past their ends.  A thread makes the pieces of
 // eight tokens of an expert.
-__global__ __launch_bounds__(kBlock) void columns_kernel(const float* dl, int64_t T, int E, int Ep,
-                                                         u32x4* out, int64_t block0) {
-  const int64_t at = (block0 + blockIdx.x) * kBlock + threadIdx.x;
+__device__ __forceinline__ void columns_piece(const float* dl, int64_t T, int E, int Ep,
+                                              u32x4* out, int64_t at) {
   const int64_t t8 = at / Ep, T32 = (T + 31) / 32;
   const int e = int(at - t8 * Ep);
   if (t8 >= T32 * 4) return;
@@ -394,10 +388,11 @@ __global__ __launch_bounds__(kBlock) void columns_kernel(const float* dl, int64_
 }
 
 // wt: the weights transposed, [Hp / 64][Ep / 32][4 tiles] blocks: rows are
-// channels, k experts; zeros past their ends.
-__global__ __launch_bounds__(kBlock) void wt_kernel(const uint16_t* w, int E, int H, int Ep,
-                                                    int64_t Hp, u32x4* out) {
-  const int64_t at = int64_t(blockIdx.x) * kBlock + threadIdx.x;
+// channels, k experts; zeros past their ends.  Row r of tile i is channel
+// (i / 2) * 32 + (r / 4) * 8 + (i % 2) * 4 + r % 4 of 64, so that a lane of the product
+// gets eight neighbours from two tiles.
+__device__ __forceinline__ void wt_piece(const uint16_t* w, int E, int H, int Ep, int64_t Hp,
+                                         u32x4* out, int64_t at) {
   const int e8 = int(at / Hp);
   const int64_t h = at - e8 * Hp;
   if (e8 * 8 >= Ep) return;
@@ -405,16 +400,28 @@ __global__ __launch_bounds__(kBlock) void wt_kernel(const uint16_t* w, int E, in
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     v[i] = h < H && e8 * 8 + i < E ? w[int64_t(e8 * 8 + i) * H + h] : 0u;
-  const int r = int(h & 3) | int((h >> 4) & 3) << 2, tile = int(h >> 2) & 3;
+  const int r = int(h & 3) | int((h >> 3) & 3) << 2;
+  const int tile = int((h >> 5) & 1) * 2 + int((h >> 2) & 1);
   out[(((h >> 6) * (Ep >> 5) + (e8 >> 2)) * 4 + tile) * kWave + (e8 & 3) * 16 + r] =
       u32x4{half(v[0], v[1]), half(v[2], v[3]), half(v[4], v[5]), half(v[6], v[7])};
+}
+
+// Both: the first `wt_blocks` workgroups make wt, the others columns.
+__global__ __launch_bounds__(kBlock) void operands_kernel(LogitsArgs a, int Ep, int64_t Hp,
+                                                          u32x4* wt, int64_t wt_blocks,
+                                                          u32x4* columns, int64_t block0) {
+  const int64_t b = block0 + blockIdx.x;
+  if (b < wt_blocks)
+    wt_piece(static_cast<const uint16_t*>(a.w), a.E, a.H, Ep, Hp, wt, b * kBlock + threadIdx.x);
+  else
+    columns_piece(a.dlogits, a.T, a.E, Ep, columns, (b - wt_blocks) * kBlock + threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------
 // dx[t, h] = sum over e of dlogits[t, e] w[e, h].  A workgroup keeps its 16 MT
 // tokens' rows of dlogits in LDS, as two bf16 parts in the order above, and
 // walks along the channels: each wave streams its share of wt, 64 channels at a
-// time, and stores 16 neighbouring channels of a token a lane.
+// time, and stores 64 bytes of a token's row by four lanes.
 // ---------------------------------------------------------------------------
 struct DxArgs {
   const float* dl;
@@ -426,7 +433,7 @@ struct DxArgs {
 };
 
 template <int MT>
-__global__ __launch_bounds__(kBlock) void dx_kernel(DxArgs g, int64_t mb0) {
+__global__ __launch_bounds__(kBlock, 2) void dx_kernel(DxArgs g, int64_t mb0) {
   extern __shared__ u32x4 rows[];            // [2 parts][Ep / 32][MT] blocks
   const int lane = lane_id(), n = lane & 15, q = lane >> 4;
   const int64_t m0 = (mb0 + blockIdx.x) * (16 * MT);
@@ -464,47 +471,60 @@ __global__ __launch_bounds__(kBlock) void dx_kernel(DxArgs g, int64_t mb0) {
   const int pairs = K32 >> 1;                // steps of 64 experts a block
   const int64_t total = int64_t(hb1 - hb0) * pairs;
   const u32x4* w = g.wt + int64_t(hb0) * K32 * (4 * kWave) + lane;
-  u32x4 b[2][2][4];
-  auto load = [&](int d, int64_t p) {
+  u32x4 b[2][2][4], a[2][2][MT];
+  auto load = [&](int d, int s, int64_t p) {
     if (p >= total) return;                  // the same for the whole wave
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int t = 0; t < 4; ++t) b[d][s][t] = w[((p * 2 + s) * 4 + t) * kWave];
+  };
+  auto read = [&](int d, int k32) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) b[d][s][t] = w[((p * 2 + s) * 4 + t) * kWave];
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) a[d][j][m] = rows[j * part + (k32 * MT + m) * kWave + lane];
   };
   f32x4 acc[MT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < 4; ++t) acc[m][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  load(0, 0);
-  load(1, 1);
+#pragma unroll
+  for (int d = 0; d < 2; ++d)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) load(d, s, d);
+  read(0, 0);
   int k = 0, hb = hb0;
   for (int64_t p0 = 0; p0 < total; p0 += 2) {
 #pragma unroll
     for (int d = 0; d < 2; ++d) {
       if (p0 + d >= total) break;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int s = 0; s < 2; ++s) {
+        // the next step's rows, which start over with every block of channels
+        read(s ^ 1, s == 0 ? 2 * k + 1 : k + 1 < pairs ? 2 * k + 2 : 0);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const u32x4 a = rows[j * part + ((2 * k + s) * MT + m) * kWave + lane];
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) acc[m][t] = mfma(b[d][s][t], a, acc[m][t]);
-          }
-      load(d, p0 + d + 2);
+            for (int t = 0; t < 4; ++t) acc[m][t] = mfma(b[d][s][t], a[s][j][m], acc[m][t]);
+        load(d, s, p0 + d + 2);
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);     // four products,
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // an LDS read
+        }
+      }
       if (++k < pairs) continue;
-      const int h = hb * 64 + q * 16;
+      const int h = hb * 64 + q * 8;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         const int64_t t = m0 + m * 16 + n;
         u32x4* to = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.dx) + t * g.H + h);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (t < g.T && h + 8 * i < g.H)
-            to[i] = u32x4{pack_bf16x2(acc[m][2 * i][0], acc[m][2 * i][1]),
+          if (t < g.T && h + 32 * i < g.H)
+            to[4 * i] = u32x4{pack_bf16x2(acc[m][2 * i][0], acc[m][2 * i][1]),
                           pack_bf16x2(acc[m][2 * i][2], acc[m][2 * i][3]),
                           pack_bf16x2(acc[m][2 * i + 1][0], acc[m][2 * i + 1][1]),
                           pack_bf16x2(acc[m][2 * i + 1][2], acc[m][2 * i + 1][3])};
@@ -671,10 +691,13 @@ hipError_t launch_router_logits_backward(const LogitsArgs& a, hipStream_t s) {
   u32x4* columns = reinterpret_cast<u32x4*>(ws + at.columns);
   u32x4* wt = reinterpret_cast<u32x4*>(ws + at.wt);
   const int Ep = int(pad64(a.E));
+  const int64_t Hp = pad64(a.H), per = kBlock;
+  const int64_t wt_blocks = a.dx ? (Hp * (Ep / 8) + per - 1) / per : 0;
+  const int64_t column_blocks = a.dw ? ((a.T + 31) / 32 * 4 * Ep + per - 1) / per : 0;
+  for_each_launch(wt_blocks + column_blocks, kBlock, [&](int64_t b0, unsigned grid) {
+    operands_kernel<<<grid, kBlock, 0, s>>>(a, Ep, Hp, wt, wt_blocks, columns, b0);
+  });
   if (a.dx) {
-    const int64_t Hp = pad64(a.H);
-    wt_kernel<<<unsigned((Hp * (Ep / 8) + kBlock - 1) / kBlock), kBlock, 0, s>>>(
-        static_cast<const uint16_t*>(a.w), a.E, a.H, Ep, Hp, wt);
     const DxShape shape = dx_shape(a.T, a.H, Ep);
     DxArgs g{};
     g.dl = a.dlogits;
@@ -693,10 +716,6 @@ hipError_t launch_router_logits_backward(const LogitsArgs& a, hipStream_t s) {
       launch_dx<4>(g, shape, s);
   }
   if (a.dw) {
-    const int64_t pieces = (a.T + 31) / 32 * 4 * Ep;
-    for_each_launch((pieces + kBlock - 1) / kBlock, kBlock, [&](int64_t b0, unsigned grid) {
-      columns_kernel<<<grid, kBlock, 0, s>>>(a.dlogits, a.T, a.E, Ep, columns, b0);
-    });
     const DwShape shape = dw_shape(a.T, a.E, a.H);
     DwArgs g{};
     g.columns = columns;
