@@ -250,7 +250,10 @@ __global__ __launch_bounds__(kBlock, 2) void logits_wide_kernel(LogitsGemm g, co
   const uint32_t off0 = uint32_t(row0) * uint32_t(pitch) + uint32_t(piece * 16);
   const uint32_t step = 32u * uint32_t(pitch);
   const bool own = n0 < g.E;                             // else the wave has no experts
-  const u32x4* w = wf + int64_t(own ? n0 >> 5 : 0) * stages * (4 * kWave) + lane;
+  // 4 KB a stage, zeros past the last: also where a weight is infinite, a stage past the
+  // end adds nothing
+  const rsrc_t wr = make_rsrc(wf + int64_t(own ? n0 >> 5 : 0) * stages * (4 * kWave),
+                              int64_t(stages) * 4096);
   u32x4 av[3][LA], wv[3][2][2];
   auto load_x = [&](int d, int i0) {
     const int st = st0 + i0;
@@ -261,12 +264,14 @@ __global__ __launch_bounds__(kBlock, 2) void logits_wide_kernel(LogitsGemm g, co
           ar, (in ? off0 : kOob) + uint32_t(i) * step, i0 < count ? st * 128 : 0, 0);
   };
   auto load_w = [&](int d, int i0) {
-    // past the end the last stage's weights meet rows of zeros
-    const u32x4* from = w + int64_t(st0 + (i0 < count ? i0 : count - 1)) * (4 * kWave);
+    const uint32_t off = i0 < count ? uint32_t(lane * 16) : kOob;
+    const int so = i0 < count ? (st0 + i0) * 4096 : 0;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) wv[d][s][t] = from[(s * 2 + t) * kWave];
+      for (int t = 0; t < 2; ++t)
+        wv[d][s][t] = __builtin_amdgcn_raw_buffer_load_b128(
+            wr, off + uint32_t((s * 2 + t) * 1024), so, 0);
   };
   auto write = [&](int d, int buf) {
 #pragma unroll

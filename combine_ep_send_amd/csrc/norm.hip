@@ -100,10 +100,11 @@ __device__ __forceinline__ u32x2 quantize_group(const double (&v)[8], const floa
     }
     return c;
   }
+  const double inverse = 1.0 / double(scale);
   uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    c[i] = scale > 0.0f ? e4m3_encode(y[i] / scale) : (y[i] != y[i] ? 0x7Fu : 0u);
+    c[i] = scale > 0.0f ? e4m3_encode(float(v[i] * inverse)) : (y[i] != y[i] ? 0x7Fu : 0u);
   return u32x2{c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
                c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24)};
 }

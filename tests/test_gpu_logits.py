@@ -89,6 +89,69 @@ def test_infinities_and_nan_stay_in_their_rows():
     assert torch.equal(dw.cpu()[4], torch.where(x[2].float() > 0, float("inf"), -float("inf")))
 
 
+@pytest.mark.parametrize("T,E,H", [(2100, 200, 328), (2100, 200, 584), (40, 20, 264)])
+def test_infinite_weights(T, E, H):
+    """An infinite weight in the last channels, whose stage ends before its products
+    do: infinities of x's sign in its expert's column, the others as they were."""
+    _, x, w = make(T, E, H, 8)
+    x[x == 0] = 1.0
+    want = ep.ep_router_logits(x.cuda(), w.cuda()).cpu()
+    w[7, H - 1], w[9, 2] = float("inf"), -float("inf")
+    got = ep.ep_router_logits(x.cuda(), w.cuda()).cpu()
+    inf = torch.tensor(float("inf"))
+    assert torch.equal(got[:, 7], torch.where(x[:, H - 1].float() > 0, inf, -inf))
+    assert torch.equal(got[:, 9], torch.where(x[:, 2].float() > 0, -inf, inf))
+    keep = [e for e in range(E) if e not in (7, 9)]
+    assert torch.equal(got[:, keep], want[:, keep])
+
+
+@pytest.mark.parametrize("T,E,H", [(70, 64, 264), (2100, 200, 328)])
+def test_arrays_aligned_to_four_bytes(T, E, H):
+    rng, x, w = make(T, E, H, 9)
+    x, w = x.cuda(), w.cuda()
+    room = torch.full((T * E + 2,), 7.0).cuda()
+    out = room[1:-1].view(T, E)
+    assert torch.equal(ep.ep_router_logits(x, w, out=out), ep.ep_router_logits(x, w))
+    assert room[0] == 7 and room[-1] == 7
+    d = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).cuda()
+    out.copy_(d)
+    for a, b in zip(ep.ep_router_logits_backward(out, x, w), ep.ep_router_logits_backward(d, x, w)):
+        assert torch.equal(a, b)
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 channels in all: the last rows as computed alone."""
+    T, E, H = 300001, 160, 7168
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_()
+    w = (torch.randn(E, H, device="cuda") / 85).bfloat16()
+    tail = slice(T - 70, T)
+    y = ep.ep_router_logits(x, w)
+    check(y[tail], *logits_ref(f64(x[tail]), f64(w)))
+    d = torch.randn(T, E, device="cuda")
+    dx, dw = ep.ep_router_logits_backward(d, x, w)
+    alone, _ = ep.ep_router_logits_backward(d[tail].contiguous(), None, w, weight_grad=False)
+    assert torch.equal(dx[tail], alone)
+    # the sums over all rows, against fp32 sums of 64-bit ones over runs of them
+    want = torch.zeros(E, H, dtype=torch.float64, device="cuda")
+    size = torch.zeros(E, H, dtype=torch.float64, device="cuda")
+    for r in torch.arange(T, device="cuda").split(20000):
+        want += d[r].double().t() @ x[r].double()
+        size += d[r].double().abs().t() @ x[r].double().abs()
+    tol = (2.0 ** -24 + (3 * T / 32 + 96) * 2.0 ** -23) * size
+    assert bool(((dw.double() - want).abs() <= tol).all())
+    del x, d, dx, y
+    n = 330000
+    s = torch.empty(n, 7168, dtype=torch.bfloat16, device="cuda").normal_()
+    g = torch.ones(7168, device="cuda")
+    a, b = ep.ep_rms_norm(s, g, fp8=True, rstd=True), ep.ep_rms_norm(s[-9:].contiguous(), g, fp8=True)
+    assert torch.equal(a.y[-9:], b.y) and torch.equal(a.scale[-9:], b.scale)
+    assert torch.equal(a.q[-9:].view(torch.uint8), b.q.view(torch.uint8))
+    back, _ = ep.ep_rms_norm_backward(s, s, g, a.rstd)
+    last, _ = ep.ep_rms_norm_backward(s[-9:].contiguous(), s[-9:].contiguous(), g,
+                                      a.rstd[-9:].contiguous())
+    assert torch.equal(back[-9:], last)
+
+
 def test_no_tokens_given_outputs_and_refusals():
     _, x, w = make(10, 12, 128, 1)
     x, w, d = x.cuda(), w.cuda(), torch.randn(10, 12).cuda()

@@ -188,6 +188,21 @@ def test_backward_against_differences(score, renorm):
     assert abs((f64(got) * v).sum() - slope) <= F32 * np.abs(f64(got) * v).sum() + 1e-8
 
 
+def test_arrays_aligned_to_four_bytes():
+    """Logits and bias off by a float: the loads of fours need 16 bytes."""
+    rng, l = logits(50, 64, 2)
+    room, bias = torch.zeros(50 * 64 + 1).cuda(), torch.zeros(65).cuda()
+    off = room[1:].view(50, 64)
+    off.copy_(torch.from_numpy(l))
+    bias[1:] = torch.from_numpy((0.1 * rng.standard_normal(64)).astype(np.float32)).cuda()
+    even = off.clone(), bias[1:].clone()
+    for kw in (dict(), dict(num_groups=4, topk_groups=2)):
+        for a, b in ((off, bias[1:]), (off, even[1]), (even[0], bias[1:])):
+            got = ep.ep_route(a, 6, score="sigmoid", bias=b, **kw)
+            want = ep.ep_route(even[0], 6, score="sigmoid", bias=even[1], **kw)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_given_outputs_and_refusals():
     _, l = logits(9, 16, 1)
     d = torch.from_numpy(l).cuda()
