@@ -37,7 +37,9 @@ inline int norm_groups(int64_t T, int H) {
   if (per_cu < 1) per_cu = 1;
   if (per_cu > 4) per_cu = 4;
   const int most = 256 * per_cu;
-  return int(T < most ? T : most);
+  // two rows or more each: a row of sums costs as much to move as a row
+  const int64_t want = (T + 1) / 2;
+  return int(want < most ? want : most);
 }
 
 // Whether rows are read with non-temporal loads: `inputs` arrays of rows that come
