@@ -14,6 +14,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -45,16 +47,25 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source into combine_ep_send_amd/libepdc.so."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    """Compile every HIP source, side by side, into combine_ep_send_amd/libepdc.so."""
     tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *srcs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    proc = subprocess.run(cmd, capture_output=True, text=True)
-    if proc.returncode != 0:
-        sys.stderr.write(proc.stdout + proc.stderr)
-        raise RuntimeError(f"hipcc failed with status {proc.returncode}")
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        proc = subprocess.run(cmd, capture_output=True, text=True)
+        if proc.returncode != 0:
+            sys.stderr.write(proc.stdout + proc.stderr)
+            raise RuntimeError(f"hipcc failed with status {proc.returncode}")
+
+    with tempfile.TemporaryDirectory() as objects:
+        objs = [os.path.join(objects, s + ".o") for s in SOURCES]
+        flags = [f for f in HIPCC_FLAGS if f != "-shared"] + ["-I", os.path.join(ROOT, "include")]
+        cc = hipcc()
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda so: run([cc, *flags, "-c", "-o", so[1],
+                                          os.path.join(CSRC, so[0])]), zip(SOURCES, objs)))
+        run([cc, *HIPCC_FLAGS, "-o", tmp, *objs])
     os.replace(tmp, LIB)
     return LIB
 

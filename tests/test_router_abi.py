@@ -62,7 +62,7 @@ def test_norm_backward_refusals():
         (dict(dw=ODD4), BAD), (dict(ws=None), WS), (dict(ws=A16), WS),
         (dict(bytes=size(2, 256) - 1), WS),
         (dict(T=0, dy=None, s=None, rstd=None, dx=None, dw=None, ws=None, bytes=0), 0)])
-    assert size(2, 256) == 2 * 256 * 4
+    assert size(2, 256) == 256 * 4 and size(64, 256) == 32 * 256 * 4
     assert size(0, 256) > 0
     for bad in ((-1, 256), (1 << 30, 256), (2, 0), (2, 12), (2, 32776), ((1 << 63) - 1, 256)):
         assert size(*bad) == 0
