@@ -96,8 +96,7 @@ inline LogitsShape logits_shape(int64_t T, int E, int H) {
   g.nb = (E + experts - 1) / experts;
   const int stages = (H + 63) / 64;
   const int64_t tiles = g.mb * g.nb;
-  // up to 64 experts a few workgroups more than compute units cost little
-  int64_t want = g.wn == 1 ? (kGemmGroups + tiles - 1) / tiles : kGemmGroups / tiles;
+  int64_t want = kGemmGroups / tiles;
   if (want < 1) want = 1;
   if (want > stages) want = stages;
   g.each = int((stages + want - 1) / want);
