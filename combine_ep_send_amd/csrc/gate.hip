@@ -116,7 +116,9 @@ __device__ __forceinline__ void store_tiles(float* to, const f32x4 (&v)[N], int 
 // from memory have neighbouring lanes in different rows, and a load of 1 KB then
 // takes 70 cycles: 129 us for 16384 tokens, 256 experts, 7168 channels.)
 // Loads go through descriptors whose range check gives zeros for rows and
-// channels past the end.
+// channels past the end.  HBM bounds it up to 64 experts (16384 tokens of 7168
+// channels 47 us, 5.0 TB/s); with 256 the L2 caches do, which give every 64 tokens
+// all the weights (99 us).
 // LDS holds a row of a stage as eight 16-byte pieces, permuted by three bits of
 // the row, so that the eight rows that a read takes at once lie in different
 // banks.  w is the instruction's first operand, so that a lane's four results are
@@ -226,7 +228,12 @@ __global__ __launch_bounds__(kBlock) void logits_kernel(LogitsGemm g, int64_t mb
 // The same for many tokens: a workgroup takes 128 of them and 128 experts, a wave all
 // the tokens and 32 experts.  The weights come in the order of the matrix cores
 // (wf_kernel), straight into registers, 1 KB a load, so that LDS moves the tokens'
-// rows alone and a weight is loaded once for 128 tokens.
+// rows alone and a weight is loaded once for 128 tokens.  16384 tokens, 256 experts,
+// 7168 channels take 80 us with the rows from HBM (264 MB, 3.3 TB/s), 57 with most of
+// them in the Infinity Cache, and 64 tokens a workgroup 99.  The rows' wait bounds
+// it: loads return in order, so a wait for weights is one for rows too.  256 experts a
+// workgroup (71 us, but then in two splits, whose sum takes 17 more) and a last
+// workgroup that adds the splits up (112: its fences write L2 back) were slower.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kBlock, 2) void logits_wide_kernel(LogitsGemm g, const u32x4* wf,
                                                                 int nb, int64_t b0) {
@@ -426,7 +433,10 @@ __global__ __launch_bounds__(kBlock) void operands_kernel(LogitsArgs a, int Ep, 
 // dx[t, h] = sum over e of dlogits[t, e] w[e, h].  A workgroup keeps its 16 MT
 // tokens' rows of dlogits in LDS, as two bf16 parts in the order above, and
 // walks along the channels: each wave streams its share of wt, 64 channels at a
-// time, and stores 64 bytes of a token's row by four lanes.
+// time, and stores 64 bytes of a token's row by four lanes.  8195 tokens, 64 experts,
+// 4096 channels take 20 us (3.4 TB/s written), 16384, 256 and 7168 118 us: 120 GFLOP
+// in two parts, 1.0 PFLOP/s of the 1.9 that products alone reach here.  Within 256
+// registers two workgroups share a compute unit (264 registers: 164 us).
 // ---------------------------------------------------------------------------
 struct DxArgs {
   const float* dl;
@@ -549,6 +559,9 @@ __global__ __launch_bounds__(kBlock, 2) void dx_kernel(DxArgs g, int64_t mb0) {
 // tokens of one channel in a lane: lane n loads eight neighbouring channels 8n..
 // of eight rows, 256 bytes of a row at a time, and swaps halves of words;
 // fragment c then holds the channels 8n + c, and a lane's results are neighbours.
+// The matrix cores bound it: 16384 tokens, 256 experts, 7168 channels take 190 us, 180
+// GFLOP in three parts, 0.95 PFLOP/s (with fragments of dlogits from rows a token
+// apart 540 us); 8195, 64 and 4096, with eight steps a wave, 20 us.
 // ---------------------------------------------------------------------------
 struct DwArgs {
   const u32x4* columns;

