@@ -361,10 +361,13 @@ __global__ __launch_bounds__(kBlock) void wf_kernel(const u32x4* w, int E, int H
 }
 
 // A float as the sum of three bf16 numbers, exact where the last is no smaller
-// than bf16 goes; what rounds to an infinity or is none has no further parts.
+// than bf16 goes.  A finite number that rounds to an infinity starts from the
+// largest finite one, 2^-8 of it away at most; infinities and NaN have no further
+// parts.
 __device__ __forceinline__ void split3(float v, uint32_t (&p)[3]) {
+  const bool fin = (__float_as_uint(v) & 0x7F800000u) != 0x7F800000u;
   p[0] = pack_bf16x2(v, 0.0f) & 0xFFFFu;
-  const bool fin = (p[0] & 0x7F80u) != 0x7F80u;
+  if (fin && (p[0] & 0x7FFFu) == 0x7F80u) p[0] -= 1u;
   const float r = fin ? v - bf16_lo(p[0]) : 0.0f;
   p[1] = pack_bf16x2(r, 0.0f) & 0xFFFFu;
   p[2] = pack_bf16x2(r - bf16_lo(p[1]), 0.0f) & 0xFFFFu;

@@ -129,7 +129,9 @@ int ep_router_logits(const void* x, const void* w, int64_t num_tokens, int num_e
  * dlogits takes part as the sum of bf16 numbers: of two for dx (off by at most
  * 2^-16 of it, beside the 2^-8 of dx's rounding), of three for dw (off by at
  * most 2^-24).  The parts are exact down to the least bf16 number: an entry
- * below 2^-109 in magnitude is off by up to 2^-133 besides.
+ * below 2^-109 in magnitude is off by up to 2^-133 besides.  Where an x or w
+ * is infinite, a sum that it enters comes out as NaN or infinite, whichever
+ * the formula gives, since one of the parts it meets may be 0.
  *
  *   dlogits    [T,E] fp32 in
  *   x, w       as above; x may be NULL when dw is, w when dx is
