@@ -437,8 +437,8 @@ __global__ __launch_bounds__(kBlock) void operands_kernel(LogitsArgs a, int Ep, 
 // tokens' rows of dlogits in LDS, as two bf16 parts in the order above, and
 // walks along the channels: each wave streams its share of wt, 64 channels at a
 // time, and stores 64 bytes of a token's row by four lanes.  8195 tokens, 64 experts,
-// 4096 channels take 20 us (3.4 TB/s written), 16384, 256 and 7168 118 us: 120 GFLOP
-// in two parts, 1.0 PFLOP/s of the 1.9 that products alone reach here.  Within 256
+// 4096 channels take 20 us (3.4 TB/s written), 16384, 256 and 7168 100 to 122 us: 120 GFLOP
+// in two parts, 1.0 to 1.2 PFLOP/s of the 1.9 that products alone reach here.  Within 256
 // registers two workgroups share a compute unit (264 registers: 164 us).
 // ---------------------------------------------------------------------------
 struct DxArgs {
@@ -562,9 +562,10 @@ __global__ __launch_bounds__(kBlock, 2) void dx_kernel(DxArgs g, int64_t mb0) {
 // tokens of one channel in a lane: lane n loads eight neighbouring channels 8n..
 // of eight rows, 256 bytes of a row at a time, and swaps halves of words;
 // fragment c then holds the channels 8n + c, and a lane's results are neighbours.
-// The matrix cores bound it: 16384 tokens, 256 experts, 7168 channels take 190 us, 180
-// GFLOP in three parts, 0.95 PFLOP/s (with fragments of dlogits from rows a token
-// apart 540 us); 8195, 64 and 4096, with eight steps a wave, 20 us.
+// The matrix cores bound it: 16384 tokens, 256 experts, 7168 channels take 174 to 206
+// us, 180 GFLOP in three parts, 0.9 to 1.0 PFLOP/s (with fragments of dlogits from rows
+// a token apart 540 us); 8195, 64 and 4096, with eight steps a wave, 20 us (with loads
+// two steps ahead 31).
 // ---------------------------------------------------------------------------
 struct DwArgs {
   const u32x4* columns;
