@@ -427,16 +427,20 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(RouteArgs a, int
   if (e >= 0)
     s = a.sigmoid ? sigmoid(double(le)) : le == -INFINITY ? 0.0 : exp_down(double(le) - most);
   if (a.renorm) total = over_lanes<16>(s, add);
-  const double each = total != 0.0 ? 1.0 / total : 0.0;
+  // no sum: no gradient, every s and slope being 0.  Quotients, since the reciprocal
+  // of a sum of sigmoids below 2^-1024 (logits below -709) is infinite; a softmax's sum
+  // is 1 or more
+  const double below = total != 0.0 ? total : 1.0;
   if (a.renorm || whole) {
-    // s / total: the weight among the chosen (renorm), or among all
-    mean = over_lanes<LANES>(d * (s * each), add);     // every lane needs it
+    // the weight among the chosen (renorm), or among all
+    const double share = s / below;
+    mean = over_lanes<LANES>(d * share, add);          // every lane needs it
     if (a.sigmoid)
-      d = (d - mean) * each;
+      d -= mean;
     else
-      d = (whole ? d : d - mean) * (s * each);
+      d = (whole ? d : d - mean) * share;
   }
-  if (a.sigmoid && e >= 0) d *= sigmoid_slope(double(le));
+  if (a.sigmoid) d = e >= 0 ? d * (sigmoid_slope(double(le)) / below) : 0.0;
   // an expert that several slots name: its first slot adds them up
   bool first = e >= 0;
   double sum = 0.0;
@@ -453,6 +457,7 @@ __global__ __launch_bounds__(kBlock) void route_backward_kernel(RouteArgs a, int
   if (first) g[e] = sum;
   __syncthreads();
   if (!live) return;
+  const double each = 1.0 / below;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int i = j * LANES + li;

@@ -205,6 +205,34 @@ def test_backward_against_differences(score, renorm):
     assert abs((f64(got) * v).sum() - slope) <= F32 * np.abs(f64(got) * v).sum() + 1e-8
 
 
+@pytest.mark.parametrize("top", [-700.0, -709.5, -712.0, -720.0, -735.0])
+def test_backward_of_sigmoids_near_the_least_number(top):
+    """Renormalised weights of scores that 64 bits only just hold: the reciprocal of
+    their sum, which 64 bits do not, takes no part.  The shares are the formula's,
+    from logits less the largest; a score's rounding to a multiple of 2^-1074 is a part
+    2^-1075 / s of it, and a share has two of them."""
+    rng = np.random.default_rng(int(-top))
+    T, E, K = 9, 24, 5
+    l = (top - 4.0 * rng.random((T, E))).astype(np.float32)
+    l[8] = -800.0                                    # a sum of 0: no gradient
+    idx = np.argsort(rng.random((T, E)), axis=1)[:, :K].astype(np.int64)
+    idx[0, 1:] = -1                                  # one slot: a constant weight
+    idx[1, 3] = idx[1, 2]
+    dw = rng.standard_normal((T, K)).astype(np.float32)
+    got = ep.ep_route_backward(torch.from_numpy(dw).cuda(), torch.from_numpy(l).cuda(),
+                               torch.from_numpy(idx).cuda(), score="sigmoid", scale=2.0)
+    ref, size = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(8):
+        ks = idx[t] >= 0
+        e, d = idx[t, ks], 2.0 * dw[t, ks].astype(np.float64)
+        q = np.exp(l[t, e].astype(np.float64) - l[t, e].max())
+        q /= q.sum()                                 # 1 - s is 1 here
+        np.add.at(ref[t], e, q * (d - (d * q).sum()))
+        np.add.at(size[t], e, q * (np.abs(d) + np.abs(d * q).sum()))
+    least = 2.0 ** -1074 / np.exp(top - 4.0)
+    check(got, ref, F32 * np.abs(ref) + (2.0 ** -44 + 4 * least) * size + SMALL)
+
+
 def test_arrays_aligned_to_four_bytes():
     """Logits and bias off by a float: the loads of fours need 16 bytes."""
     rng, l = logits(50, 64, 2)
