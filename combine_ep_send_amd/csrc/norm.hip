@@ -62,11 +62,11 @@ __device__ __forceinline__ void load_weight(const void* weight, int j, float (&w
 
 // e4m3 codes and scale of 128 values held by 16 lanes, 8 each, in 64 bits (v) and
 // rounded to fp32 (y): the rules of the dispatch's fp8 rows, the quotient rounded
-// once.  v / scale is v times 1 / scale in 64 bits, one division for the lane.  NaN is left out of amax; only a lane with one, or
-// a group with an infinity, needs the encoder that knows NaN.  A quotient passes
-// 448 by 2^-23 of it, or by more where the scale is subnormal; past 464 the
-// conversion instruction gives NaN, so the quotients are clamped first, which
-// is the saturation the codes call for.
+// once.  v / scale is v times 1 / scale in 64 bits, one division for the lane.  NaN is
+// left out of amax; only a lane with one, or a group with an infinity, needs the
+// encoder that knows NaN.  A quotient passes 448 by 2^-23 of it, or by more where the
+// scale is subnormal; past 464 the conversion instruction gives NaN, so the quotients
+// are clamped first, which is the saturation the codes call for.
 __device__ __forceinline__ u32x2 quantize_group(const double (&v)[8], const float (&y)[8],
                                                 bool pow2, float& scale) {
   uint32_t m = 0u;
@@ -112,10 +112,9 @@ __device__ __forceinline__ u32x2 quantize_group(const double (&v)[8], const floa
 // ---------------------------------------------------------------------------
 // Forward: one workgroup a row, the row in registers between the sum of squares
 // and the output, so that every byte moves once.  The squares of eight neighbours
-// add up in fp32, the rest of the row's sum in 64 bits, and so are the values that
-// become codes (Q): the codes are then the roundings of the formula's values but for
-// about one in 10^7, instead of one in 10^5, at the same speed (a value that goes to
-// bf16 alone is in fp32).  16384 rows of 7168 channels with residual and codes: 171 to
+// add up in fp32, the rest of the row's sum in 64 bits (all of it there: 205 against
+// 185 us), and the values that become codes (Q) are in 64 bits, at the same speed (a
+// value that goes to bf16 alone is in fp32).  16384 rows of 7168 channels with residual and codes: 171 to
 // 195 us (1061 MB, 5.4 to 6.2 TB/s).  A thread's pieces lie a
 // workgroup apart: consecutive threads move consecutive 16-byte pieces, and 16
 // neighbours hold a 128-channel group.
@@ -164,9 +163,30 @@ __global__ __launch_bounds__(kNormMaxThreads) void rms_norm_kernel(NormArgs a) {
       for (int k = 0; k < 8; ++k) s = __builtin_fmaf(f[k], f[k], s);
       sum += double(s);
     }
-    const double rstd =
-        1.0 / sqrt(block_sum(sum, part[turn]) / double(a.H) + double(a.eps));
+    sum = block_sum(sum, part[turn]);
+    // Squares that fp32 does not hold are taken once more in 64 bits: below 2^-100 for the
+    // row (its additions are off by up to 2^-150 each, by 2^-135 in all) or infinite.  The
+    // same in the whole workgroup.
+    const double all_eps = double(a.H) * double(a.eps);
+    if (!(sum + all_eps >= 0x1p-100 && sum < INFINITY)) {
+      turn ^= 1;
+      sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < PT; ++i) {
+        // unpacked anew, or the floats would take registers up to here in every row
+        asm volatile("" : "+v"(v[i]));
+        float f[8];
+        unpack8(v[i], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum = __builtin_fma(double(f[k]), double(f[k]), sum);
+      }
+      sum = block_sum(sum, part[turn]);
+    }
+    const double rstd = 1.0 / sqrt((sum + all_eps) / double(a.H));
     if (a.rstd && threadIdx.x == 0) a.rstd[t] = float(rstd);
+    // without codes y is in fp32; the least rows' rstd, up to 2^141, is past it
+    const float lift = rstd > 0x1p120 ? 0x1p21f : 1.0f;
+    const float rstd32 = float(rstd > 0x1p120 ? rstd * 0x1p-21 : rstd);
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
       const int j = i * n + int(threadIdx.x);
@@ -181,7 +201,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void rms_norm_kernel(NormArgs a) {
           y[k] = double(f[k]) * rstd * double(w[k]);
           f[k] = float(y[k]);
         } else {
-          f[k] = f[k] * float(rstd) * w[k];
+          f[k] = f[k] * lift * rstd32 * w[k];
         }
       }
       if (a.out) st_stream(static_cast<u32x4*>(a.out) + t * H8 + j, pack8(f));

@@ -47,9 +47,11 @@ typedef enum { EP_NORM_W_BF16 = 0, EP_NORM_W_F32 = 1 } ep_norm_weight_t;
  *   q, scale: e4m3 codes and one scale per 128 channels of y, not of out: amax =
  *             max |fp32(y)|, scale = fp32(amax / 448), or the smallest power of
  *             two at or above that, code = e4m3(fp32(y / scale)).
- * rstd is in 64 bits, from fp32 sums of the squares of eight neighbours (a sum past
- * fp32, channels of 2^62 and more, makes it 0); y is in 64 bits where there are
- * codes, in fp32 without.
+ * rstd is in 64 bits, from fp32 sums of the squares of eight neighbours, or from 64-bit
+ * squares where fp32 does not hold the row's (below 2^-100 with H * eps, or past its
+ * largest); y is in 64 bits where there are codes, in fp32 without.  The rstd that is
+ * written is infinite where fp32 cannot hold it: rows whose root mean square lies below
+ * 2^-128, with an eps as small.
  * The rounding of the codes, saturation, zeros, NaN and infinities follow
  * ep_dispatch_permute's fp8 form.  A group whose scale is 0 (amax below
  * 448 * 2^-150) has codes 0.
@@ -84,7 +86,7 @@ size_t ep_rms_norm_backward_workspace_bytes(int64_t num_tokens, int hidden);
  *   dx[t,:]    = bf16( rstd * (g - n * mean(g * n)) + d_residual[t,:] )
  *   dweight[h] = sum over t of dy[t,h] * n[t,h]     (fp32)
  * dx is the gradient of x and of the residual alike.  The gradient passes the
- * 8-bit output's rounding as if there were none.
+ * 8-bit output's rounding as if there were none.  A row whose rstd is infinite has NaN.
  *
  *   dy          [T,H] bf16 in: the gradient of y (16-byte aligned)
  *   s           [T,H] bf16 in: residual_out, or x without a residual

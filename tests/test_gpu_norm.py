@@ -109,6 +109,73 @@ def test_rows_of_zeros_infinities_and_nan():
     assert (tiny.q.float() == 352).all()            # 350 between 320 and 352
 
 
+# mean squares that fp32 cannot hold, or holds in few bits; a bf16 number's square is
+# exact in 64 bits
+SIZES = [2.0 ** -132, 2.0 ** -110, 2.0 ** -80, 2.0 ** -75, 2.0 ** -70, 2.0 ** -66, 2.0 ** -50,
+         2.0 ** 58, 2.0 ** 62, 2.0 ** 64, 2.0 ** 100, 2.0 ** 120]
+
+
+@pytest.mark.parametrize("H", [8, 256, 640, 7168, 12288, 32768])
+@pytest.mark.parametrize("f32", [False, True])
+def test_rows_of_every_size_without_eps(H, f32):
+    """eps = 0 divides rows of every size by their own: y near the weight, whatever
+    the size, with codes and without."""
+    rng, x, _, w = make(len(SIZES), H, H, f32, False)
+    x = bf16(f64(x) / np.sqrt((f64(x) ** 2).mean(1, keepdims=True)) *
+             np.array(SIZES)[:, None])               # bf16's own least steps at the first
+    least = torch.zeros(1, H, dtype=torch.bfloat16)
+    least[0, H // 2] = TINY                          # the largest rstd there is
+    x = torch.cat((x, least))
+    fp8 = H % 128 == 0
+    n = ep.ep_rms_norm(x.cuda(), w.cuda(), 0.0, fp8=fp8, rstd=True)
+    rstd, rtol, y, tol = norm_ref(f64(x), f64(w), 0.0)
+    held = rstd < torch.finfo(torch.float32).max     # the least rows' is past fp32
+    assert held.sum() >= len(SIZES) - 1 and not held[-1]
+    # the largest rows' is subnormal in fp32
+    check(f64(n.rstd)[held], rstd[held], rtol[held] + 2.0 ** -150, "rstd")
+    assert np.isinf(f64(n.rstd)[~held]).all()
+    for got in (n.y, ep.ep_rms_norm(x.cuda(), w.cuda(), 0.0).y):
+        check(got, y, tol + BF16 * np.abs(y) + TINY, "y")
+    if fp8:
+        scale = f64(n.scale)
+        near = (tol / np.maximum(np.abs(y), 1e-30)).max() + 2 * F32
+        amax = np.abs(y).reshape(len(x), -1, 128).max(-1) / 448
+        check(scale, amax, amax * near, "scale")
+
+
+@pytest.mark.parametrize("H", [256, 7168])
+def test_backward_of_rows_of_every_size(H):
+    """The first size's rstd is past fp32."""
+    sizes = np.array(SIZES[1:])
+    rng, s, _, w = make(len(sizes), H, H + 9, True, False)
+    s = bf16(f64(s) / np.sqrt((f64(s) ** 2).mean(1, keepdims=True)) * sizes[:, None])
+    dy = bf16(rng.standard_normal(s.shape))
+    n = ep.ep_rms_norm(s.cuda(), w.cuda(), 0.0, rstd=True)
+    dx, dw = ep.ep_rms_norm_backward(dy.cuda(), s.cuda(), w.cuda(), n.rstd)
+    rx, tx, rw, tw = norm_backward_ref(f64(dy), f64(s), f64(w), f64(n.rstd))
+    check(dx, rx, tx, "dx")
+    check(dw, rw, tw, "dw")
+
+
+def test_rows_of_every_size_in_turn():
+    """More rows than workgroups: a workgroup of two waves takes an ordinary row and
+    then one of another size, or the other way round."""
+    T, H = (1 << 20) + 4096, 520
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x = torch.randn(T, H, device="cuda", generator=g)
+    x *= torch.tensor([1.0, 2.0 ** -80, 2.0 ** 70, 2.0 ** -68, 3.0], device="cuda")[
+        torch.arange(T, device="cuda") % 5, None]    # 2^20 leaves 1 over 5: sizes differ
+    x = x.to(torch.bfloat16)
+    w = torch.ones(H, device="cuda")
+    n = ep.ep_rms_norm(x, w, 0.0)
+    for r in torch.arange(T, device="cuda").split(1 << 17):
+        s = x[r].double()
+        y = s * s.square().mean(1, keepdim=True).rsqrt()
+        # 64-bit values, or fp32 sums of eight squares, then two roundings
+        assert bool(((n.y[r].double() - y).abs() <= (BF16 + 16 * F32) * y.abs()).all())
+
+
 def test_in_place_and_given_outputs():
     _, x, r, w = make(33, 1024, 5, False)
     x, r, w = x.cuda(), r.cuda(), w.cuda()
