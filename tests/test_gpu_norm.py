@@ -176,6 +176,20 @@ def test_rows_of_every_size_in_turn():
         assert bool(((n.y[r].double() - y).abs() <= (BF16 + 16 * F32) * y.abs()).all())
 
 
+def test_rows_with_codes_and_without():
+    """y from 64-bit values beside codes, from fp32 ones (four roundings) without: one
+    bf16 step apart where a value lies that close to the border of two."""
+    _, x, _, w = make(512, 2048, 14, True, False)
+    a, b = (f64(ep.ep_rms_norm(x.cuda(), w.cuda(), fp8=fp8).y) for fp8 in (True, False))
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(a), np.abs(b)) + TINY)) - 7)
+    assert (np.abs(a - b) <= step).all()
+    # a border every 2^-8, at most 4 F32 of a value's size to either side of it
+    assert (a != b).mean() < 2 * 8 * F32 / BF16
+    both = a != b
+    _, _, y, _ = norm_ref(f64(x), f64(w), float(np.float32(1e-6)))
+    assert (np.abs(a - y)[both] <= (BF16 + F32) * np.abs(y)[both]).all()
+
+
 def test_in_place_and_given_outputs():
     _, x, r, w = make(33, 1024, 5, False)
     x, r, w = x.cuda(), r.cuda(), w.cuda()
