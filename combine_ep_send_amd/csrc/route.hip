@@ -249,14 +249,23 @@ __global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width, b
                                                          int64_t block0) {
   constexpr int kTokens = kBlock / LANES;
   const int li = int(threadIdx.x) & (LANES - 1);
-  const int64_t t = (block0 + blockIdx.x) * kTokens + int(threadIdx.x) / LANES;
+  const int64_t t0 = (block0 + blockIdx.x) * kTokens;
+  const int64_t t = t0 + int(threadIdx.x) / LANES;
+  const int64_t all = a.token_count ? route_live(a.T, a.token_count[0]) : a.T;
+  if (t0 >= all) {                     // padding throughout, for the whole workgroup
+    if (t < a.T && li < a.K) {
+      a.topk_idx[t * a.K + li] = -1;
+      a.topk_weights[t * a.K + li] = 0.0f;
+    }
+    return;
+  }
   // every lane takes part in the moves; only the loads and stores are masked
-  const bool live = t < a.T && (!a.token_count || t < a.token_count[0]);
+  const bool live = t < all;
   const int size = a.E / a.groups;
   const int g = li / width, first = li & (width - 1);
   // every place is loaded, so that the loads go out together; what is none of
-  // the token's (a token past the end loads the last one's) becomes -infinity
-  const float* row = a.logits + (t < a.T ? t : a.T - 1) * a.E;
+  // the token's (one past the last loads the last one's) becomes -infinity
+  const float* row = a.logits + route_row(t, all) * a.E;
   // place of the lane's j-th expert in its group: fours have steps of 1 inside
   const int base = g * size + (fours ? 4 * first : first), inside = fours ? 1 : width;
   auto expert = [&](int j) { return base + (j & 3) * inside + (j >> 2) * 4 * width; };

@@ -71,6 +71,13 @@ inline RouteShape route_shape(int E, int groups) {
   }
 }
 
+// Tokens that take part, by the padding's `count`; and the token whose logits are read
+// in t's place: no logits of a padding token are, nor any where there are none else.
+constexpr int64_t route_live(int64_t T, int64_t count) {
+  return count < 0 ? 0 : count < T ? count : T;
+}
+constexpr int64_t route_row(int64_t t, int64_t live) { return t < live ? t : live - 1; }
+
 // ---- the router's products -----------------------------------------------------
 constexpr int kGemmGroups = 256;      // workgroups that fill the chip
 

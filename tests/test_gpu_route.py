@@ -149,6 +149,27 @@ def test_padding_tokens_are_not_routed():
         check(w, rw, np.abs(rw) * F32 * 1.001 + SMALL)
 
 
+@pytest.mark.parametrize("E,G", [(24, 1), (64, 4), (600, 1), (1024, 8)])
+def test_workgroups_of_padding(E, G):
+    """Counts inside a workgroup's tokens (16, or 4 past 256 experts), at their ends and
+    with whole workgroups behind them; what the outputs held is overwritten."""
+    rng, l = logits(70, E, E)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    d, b = torch.from_numpy(l).cuda(), torch.from_numpy(bias).cuda()
+    kw = dict(score="sigmoid", bias=b, num_groups=G, topk_groups=max(1, G // 2))
+    want_idx, want_w = ep.ep_route(d, 5, **kw)
+    for count in (-3, 0, 1, 3, 4, 5, 15, 16, 17, 31, 32, 64, 69, 70, 71):
+        n = min(70, max(0, count))
+        pad = d.clone()
+        pad[n:] = float("nan")
+        idx = torch.full((70, 5), 77, device="cuda")
+        w = torch.full((70, 5), 7.0, device="cuda")
+        ep.ep_route(pad, 5, token_count=torch.tensor([count], dtype=torch.int32).cuda(),
+                    topk_idx=idx, topk_weights=w, **kw)
+        assert torch.equal(idx[:n], want_idx[:n]) and torch.equal(w[:n], want_w[:n]), count
+        assert bool((idx[n:] == -1).all()) and bool((w[n:] == 0).all()), count
+
+
 @pytest.mark.parametrize("E,K", [(1, 1), (8, 2), (60, 4), (127, 16), (256, 8), (300, 8), (1024, 16)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
