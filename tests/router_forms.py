@@ -63,6 +63,15 @@ def logits_ref(x, w):
     return x @ w.T, (H / 32 + 32 + 4 + 256) * STEP * (np.abs(x) @ np.abs(w).T) + SMALL
 
 
+# sizes with several turns of every product's ring of stages, the last turn not whole,
+# and several workgroups of experts: by logits_shape 64 tokens by 64, 128 and 256
+# experts, 16 and 32 tokens by 256, 128 by 128 in the wide form; by dx_shape 64, 32 and
+# 16 tokens.  tests/test_router_rules.py holds them to that.
+DEEP = [(8195, 64, 1032), (8200, 128, 648), (2000, 256, 4872), (2047, 300, 1672), (1000, 700, 1096),
+        (17, 1024, 65536), (16, 1024, 16392), (9001, 129, 648), (8195, 300, 648), (2100, 1000, 456),
+        (4099, 513, 840), (2048, 400, 1032)]
+
+
 def logits_backward_ref(dl, x, w):
     T, E = dl.shape
     dx, dw = dl @ w, dl.T @ x

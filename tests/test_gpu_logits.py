@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import combine_ep_send_amd as ep
-from tests.router_forms import bf16, check, f64, logits_backward_ref, logits_ref
+from tests.router_forms import DEEP, bf16, check, f64, logits_backward_ref, logits_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -44,6 +44,37 @@ def test_backward(T, E, H):
     assert none is None and torch.equal(only, dx)
     none, only = ep.ep_router_logits_backward(d, x.cuda(), None, input_grad=False)
     assert none is None and torch.equal(only, dw)
+
+
+@pytest.mark.parametrize("T,E,H", DEEP)
+def test_many_stages_are_exact(T, E, H):
+    """Whole numbers whose sums of magnitudes fit fp32's 24 bits: equal to the bit in
+    whatever order, so that a stage taken twice, left out or read too early shows."""
+    rng = np.random.default_rng(T + E + H)
+    x, w = (rng.integers(-8, 9, (n, H)).astype(np.float64) for n in (T, E))
+    assert 64 * H < 1 << 24
+    got = ep.ep_router_logits(bf16(x).cuda(), bf16(w).cuda())
+    assert np.array_equal(f64(got), x @ w.T)
+    # 12 bits: two bf16 parts
+    d = rng.integers(-(1 << 11), (1 << 11) + 1, (T, E)).astype(np.float64)
+    x[rng.random((T, H)) < 0.9] = 0.0
+    x, w = np.sign(x), np.clip(w, -2, 2)
+    assert (np.abs(d).T @ np.abs(x)).max() < 1 << 24 and 4096 * E < 1 << 24
+    dx, dw = ep.ep_router_logits_backward(torch.from_numpy(d).float().cuda(), bf16(x).cuda(),
+                                          bf16(w).cuda())
+    assert torch.equal(dx.cpu(), bf16(d @ w))
+    assert np.array_equal(f64(dw), d.T @ x)
+
+
+@pytest.mark.parametrize("T,E,H", DEEP)
+def test_many_stages(T, E, H):
+    rng, x, w = make(T, E, H, T + 2 * E + H)
+    check(ep.ep_router_logits(x.cuda(), w.cuda()), *logits_ref(f64(x), f64(w)))
+    dl = (rng.standard_normal((T, E)) * rng.uniform(0.01, 10, (T, 1))).astype(np.float32)
+    dx, dw = ep.ep_router_logits_backward(torch.from_numpy(dl).cuda(), x.cuda(), w.cuda())
+    rx, tx, rw, tw = logits_backward_ref(dl.astype(np.float64), f64(x), f64(w))
+    check(dx, rx, tx, "dx")
+    check(dw, rw, tw, "dw")
 
 
 def test_small_numbers_are_exact():

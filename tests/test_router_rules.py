@@ -9,6 +9,7 @@ import subprocess
 import pytest
 
 from tests.expert_forms import CSRC
+from tests.router_forms import DEEP
 
 pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not found")
 
@@ -17,6 +18,14 @@ RULES = r"""
 using namespace epdc;
 extern "C" int64_t live(int64_t T, int64_t count) { return route_live(T, count); }
 extern "C" int64_t row(int64_t t, int64_t live) { return route_row(t, live); }
+extern "C" void forms(int64_t T, int E, int H, int64_t* f) {
+  const LogitsShape g = logits_shape(T, E, H);
+  f[0] = g.wide, f[1] = g.bm, f[2] = g.wn, f[3] = g.nb, f[4] = g.each, f[5] = g.splits;
+  const DxShape x = dx_shape(T, H, int(pad64(E)));
+  f[6] = x.mt, f[7] = x.mb, f[8] = x.each;
+  const DwShape w = dw_shape(T, E, H);
+  f[9] = w.eb, f[10] = w.splits, f[11] = w.each;
+}
 """
 
 
@@ -32,7 +41,35 @@ def rules(tmp_path_factory):
     for name in ("live", "row"):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int64, [ctypes.c_int64, ctypes.c_int64]
+    lib.forms.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
     return lib
+
+
+def test_every_product_is_tested_over_many_stages(rules):
+    """DEEP reaches each form of the logits with more stages a workgroup than its ring of
+    three and a turn that is not whole, each that splits the channels or not, and several
+    workgroups of experts; the rows' gradient in each of its sizes over several workgroups
+    and blocks of channels; the weights' in several parts and steps."""
+    logits, split, experts, dx, dw = set(), set(), set(), set(), set()
+    for T, E, H in DEEP:
+        f = (ctypes.c_int64 * 12)()
+        rules.forms(T, E, H, f)
+        wide, bm, wn, nb, each, splits, mt, mb, dx_each, eb, dw_splits, dw_each = f
+        form = "wide" if wide else (bm, wn)
+        if each > 3 and each % 3:
+            logits.add(form)
+            split.add((form, splits > 1))
+        if nb > 2 or (nb > 1 and not wide):
+            experts.add(form)
+        if T > 16 * mt and mb > 1 and dx_each > 4:
+            dx.add(mt)
+        dw.add((eb > 1, dw_splits > 1, dw_each > 4))
+    assert logits == {(64, 1), (64, 2), (64, 4), (32, 4), (16, 4), "wide"}
+    assert split >= {((64, 1), False), ((64, 2), False), ((64, 4), True), ((32, 4), True),
+                     ((16, 4), True), ("wide", False), ("wide", True)}
+    assert experts >= {(64, 4), (32, 4), (16, 4), "wide"}
+    assert dx == {1, 2, 4}
+    assert dw >= {(False, True, True), (True, True, True), (True, False, False)}
 
 
 @pytest.mark.parametrize("tokens", [4, 16])
