@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import combine_ep_send_amd as ep
-from tests.router_forms import BF16, TINY, bf16, check, f64, permute_ref, route_ref
+from tests.router_forms import (BF16, TINY, bf16, check, f64, logits_backward_ref,
+                                norm_backward_ref, permute_ref, route_ref)
 
 pytestmark = pytest.mark.gpu
 FP8 = torch.float8_e4m3fn
@@ -205,6 +206,91 @@ def test_training_step_against_autograd():
     check(dx, rx, BF16 * np.abs(rx) + 200 * 2.0 ** -24 * (g + m * (1 + g.mean(1, keepdims=True))) * 4)
     check(d_weight, f64(weight.grad),
           300 * 2.0 ** -24 * np.abs(f64(d_y) * f64(n.residual) * f64(n.rstd)[:, None]).sum(0))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_every_gradient_of_a_step(score, renorm):
+    """As the step above, with experts that differ: each destination scales its rows by a
+    power of two of its own (exact in bf16), so that renormalised weights have a gradient
+    too.  Every gradient is far larger than its bound, so that zeros, another scale or a
+    share left out would not pass.  The last tokens are padding."""
+    T, H, E, K, P, live = 90, 256, 32, 4, 8, 84
+    f = Front(T, H, E, K, P, 6, False)
+    factor = torch.tensor([1.0, -2.0, 0.5, 4.0, -1.0, 2.0, -0.5, 1.0]).cuda()
+    how = dict(score=score, renormalize=renorm, scale=1.5)
+    n = ep.ep_rms_norm(f.x, f.weight, residual=f.residual, rstd=True)
+    logits = ep.ep_router_logits(n.y, f.gate)
+    idx, w = ep.ep_route(logits, K, bias=f.bias, num_groups=4, topk_groups=2,
+                         token_count=torch.tensor([live], dtype=torch.int32).cuda(), **how)
+    recv, _, _, handle = ep.dispatch(n.y, idx, w, num_local_experts=E // P, num_ranks=P)
+    by = factor[handle.send_rank.long()][:, None].bfloat16()
+    local = recv * by
+    out = ep.combine(local, handle)
+    dout = bf16(np.random.default_rng(2).standard_normal((T, H))).cuda()
+    d_local, d_w = ep.combine_backward(dout, local, handle)
+    d_logits = ep.ep_route_backward(d_w, logits, idx, **how)
+    d_router, d_gate = ep.ep_router_logits_backward(d_logits, n.y, f.gate)
+    d_y = ep.ep_combine(d_local * by, handle.token_row, None, bias=d_router)
+
+    y = n.y.double().cpu().requires_grad_()
+    gate = f.gate.double().cpu().requires_grad_()
+    some = torch.arange(T)[:, None] < live
+    at = idx.cpu().clamp(min=0)
+    assert torch.equal(idx.cpu() >= 0, some.expand(T, K))
+    l = y @ gate.t()
+    s = (torch.sigmoid(l) if score == "sigmoid" else torch.softmax(l, 1)).gather(1, at)
+    wt = 1.5 * s / s.sum(1, keepdim=True) if renorm else 1.5 * s
+    for t in (l, wt):
+        t.retain_grad()
+    scale = factor.double().cpu()[at // (E // P)] * some
+    res = (wt * scale).sum(1, keepdim=True) * y
+    (res * dout.double().cpu()).sum().backward()
+
+    def seen(ref, tol):
+        # half of them at least: tokens whose experts share a factor have no gradient
+        # where weights are renormalised
+        part = float((np.abs(ref) > 10 * tol).mean())
+        assert part > 0.5
+    weights, ys, gs = f64(wt.detach()), np.abs(f64(n.y)), np.abs(f64(f.gate))
+    fs = np.abs(scale.numpy())
+    # a row's factor is exact; up to K rows are added in fp32 and rounded once
+    check(out, f64(res.detach()), BF16 * np.abs(f64(res.detach())) +
+          8 * 2.0 ** -24 * (weights * fs).sum(1, keepdims=True) * ys + TINY, "out")
+    # sums of H products in fp32
+    e = 300 * 2.0 ** -24 * (np.abs(f64(dout)) * ys).sum(1, keepdims=True)
+    check(d_w, f64(wt.grad), e * fs + 1e-30, "d_w")
+    seen(f64(wt.grad)[:live], (e * fs)[:live])
+    # a weight's share of its logit's gradient is at most scale, twice: its own and the mean's
+    worst = 3 * e * fs.max(1, keepdims=True)
+    tol = worst + 2.0 ** -24 * np.abs(f64(l.grad))
+    check(d_logits, f64(l.grad), tol, "d_logits")
+    seen(f64(l.grad.gather(1, at))[:live], tol[:live].max(1, keepdims=True))
+    # the router's products from the d_logits that reached them, and with that one's bound
+    # against autograd
+    rx, tx, rw, tw = logits_backward_ref(f64(d_logits), f64(n.y), f64(f.gate))
+    check(d_gate, rw, tw, "d_gate")
+    seen(rw, tw)
+    check(d_gate, f64(gate.grad), tw + np.broadcast_to(tol, (T, E)).T @ ys, "d_gate by autograd")
+    # the router's share, rounded to bf16 (in tx); a destination's rows, each rounded to
+    # bf16; their sum in fp32, rounded
+    ref, size = rx.copy(), np.abs(rx)
+    for r in range(P):
+        hit = (at.numpy() // (E // P) == r) & some.numpy()
+        row = (weights * scale.numpy() * hit).sum(1, keepdims=True) * f64(dout)
+        ref, size = ref + row, size + np.abs(row)
+    near = tx + BF16 * 1.01 * size + BF16 * np.abs(ref) + TINY
+    check(d_y, ref, near, "d_y")
+    seen(ref[:live], near[:live])
+    seen(rx[:live], 0.3 * near[:live])
+    check(d_y, f64(y.grad), near + np.broadcast_to(tol, (T, E)) @ gs, "d_y by autograd")
+    # the norm's, from the d_y that reached it
+    dx, d_weight = ep.ep_rms_norm_backward(d_y, n.residual, f.weight, n.rstd, d_residual=dout)
+    rx, tx, rw, tw = norm_backward_ref(f64(d_y), f64(n.residual), f64(f.weight), f64(n.rstd),
+                                       f64(dout))
+    check(dx, rx, tx, "dx")
+    check(d_weight, rw, tw, "d_weight")
+    seen(rw, tw)
 
 
 def test_layer_of_a_few_tokens():
