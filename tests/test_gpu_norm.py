@@ -265,6 +265,37 @@ def test_gradient_against_differences():
     assert abs(got - slope) <= 1.1 * BF16 * np.abs(f64(dx) * v).sum() + 1e-5
 
 
+@pytest.mark.parametrize("H", [512, 4104])
+def test_gradient_of_a_cotangent_along_the_row(H):
+    """Cotangents close to the normalised row, so that dx is what the mean leaves of a ten
+    times larger g: along the row nothing (y does not change with the row's size, but
+    for eps), along others what central differences of the formula in 64 bits give, their
+    error of third order in the step.  Row by row, within dx's rounding, which dx without
+    the mean's term, or with its other sign, is far outside of."""
+    rng, s, _, w = make(6, H, H + 2, True, False)
+    w64, eps = f64(w), float(np.float32(1e-6))
+    n = ep.ep_rms_norm(s.cuda(), w.cuda(), 1e-6, rstd=True)
+    s64, rstd = f64(s), f64(n.rstd)[:, None]
+    c = bf16(s64 * rstd / w64 + 0.1 * rng.standard_normal((6, H)))
+    dx, _ = ep.ep_rms_norm_backward(c.cuda(), s.cuda(), w.cuda(), n.rstd)
+    dx, c = f64(dx), f64(c)
+    term = rstd * s64 * rstd * (c * w64 * s64 * rstd).mean(1, keepdims=True)
+
+    def value(a):
+        return (c * w64 * a / np.sqrt((a * a).mean(1, keepdims=True) + eps)).sum(1)
+    for v in (s64, rng.standard_normal((6, H)) / rstd):
+        h = 1e-5
+        slope = (value(s64 + h * v) - value(s64 - h * v)) / (2 * h)
+        # dx's rounding to bf16; fp32 roundings of the two terms it is the difference of,
+        # 92 additions for the mean's; the differences' own: 64-bit values over the step
+        tol = BF16 * np.abs(dx * v).sum(1) + 100 * F32 * np.abs(term * v).sum(1) + \
+            2.0 ** -50 * np.abs(c * w64 * s64 * rstd).sum(1) / h + 1e-8 * np.abs(c * v).sum(1)
+        assert (np.abs((dx * v).sum(1) - slope) <= tol).all()
+        for wrong in (dx + term, dx + 2 * term):
+            assert (np.abs((wrong * v).sum(1) - slope) > 5 * tol).any()
+    assert (np.abs(((dx + term) * s64).sum(1)) > 50 * BF16 * np.abs(dx * s64).sum(1)).all()
+
+
 def test_refusals():
     x = torch.zeros(4, 256, dtype=torch.bfloat16).cuda()
     w = torch.ones(256).cuda()
