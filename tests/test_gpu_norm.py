@@ -228,6 +228,42 @@ def test_backward(T, H, f32, residual):
     assert none is None and torch.equal(alone, got)
 
 
+@pytest.mark.parametrize("H,f32", [(4096, False), (8192, True), (12288, False), (24576, True)])
+def test_rows_past_the_cache(H, f32):
+    """Inputs of 384 MiB and more, which are read past the caches, with a residual: every
+    row as a call of few rows gives it, rows at both ends against 64 bits."""
+    T = (384 << 20) // (4 * H) + 5
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H)
+    x, r, dy = (torch.randn(T, H, device="cuda", generator=g).bfloat16() for _ in range(3))
+    w = 1 + 0.3 * torch.randn(H, device="cuda", generator=g)
+    w = w if f32 else w.bfloat16()
+    few = [slice(a, min(a + 2000, T)) for a in range(0, T, 2000)]
+    for fp8 in (False, True):
+        n = ep.ep_rms_norm(x, w, 1e-5, residual=r, fp8=fp8, rstd=True)
+        for b in few:
+            m = ep.ep_rms_norm(x[b], w, 1e-5, residual=r[b], fp8=fp8, rstd=True)
+            assert torch.equal(n.residual[b], m.residual) and torch.equal(n.rstd[b], m.rstd)
+            assert torch.equal(n.y[b], m.y)
+            if fp8:
+                assert torch.equal(n.q[b].view(torch.uint8), m.q.view(torch.uint8))
+                assert torch.equal(n.scale[b], m.scale)
+        for b in (slice(0, 2), slice(T - 2, T)):
+            s = (x[b].float() + r[b].float()).bfloat16()
+            assert torch.equal(n.residual[b], s)
+            _, _, y, tol = norm_ref(f64(s), f64(w), float(np.float32(1e-5)))
+            check(n.y[b], y, tol + BF16 * np.abs(y) + TINY, "y")
+    dx, dw = ep.ep_rms_norm_backward(dy, n.residual, w, n.rstd, d_residual=r)
+    want, size = (torch.zeros(H, dtype=torch.float64, device="cuda") for _ in range(2))
+    for b in few:
+        m, _ = ep.ep_rms_norm_backward(dy[b], n.residual[b], w, n.rstd[b], d_residual=r[b])
+        assert torch.equal(dx[b], m)
+        part = dy[b].double() * n.residual[b].double() * n.rstd[b].double()[:, None]
+        want, size = want + part.sum(0), size + part.abs().sum(0)
+    # as in norm_backward_ref
+    assert bool(((dw - want).abs() <= (T / 256 + 86) * F32 * size).all())
+
+
 def test_backward_in_place_and_no_tokens():
     rng, s, _, w = make(50, 264, 8, False, False)
     dy, dr = bf16(rng.standard_normal((50, 264))).cuda(), bf16(rng.standard_normal((50, 264))).cuda()

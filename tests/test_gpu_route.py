@@ -106,6 +106,29 @@ def test_neighbouring_logits_are_told_apart():
             against(l, 16, np.zeros(64, np.float32), score="sigmoid")
 
 
+@pytest.mark.parametrize("base", [8.0, 13.0, -20.0, -80.0])
+def test_neighbouring_large_logits_are_told_apart(base):
+    """Sigmoids of logits one fp32 step apart: up to 13 they differ by 2^-39 and more, and
+    keys are held to 2^-43 below 1; negative ones by 2^-20 of their size."""
+    steps = np.arange(64, dtype=np.int32)
+    l = (np.float32(base).view(np.int32) + steps).view(np.float32)[None].repeat(2, 0).copy()
+    l[1] = l[1, ::-1]
+    against(l, 16, np.zeros(64, np.float32), score="sigmoid")
+    against(l, 16, score="sigmoid")
+    against(l, 16, score="sigmoid", num_groups=4, topk_groups=2)
+
+
+def test_saturated_sigmoids_are_equal_keys():
+    """From 40 on a sigmoid is 1 in 64 bits: with a bias the lowest numbers win, without one
+    the logits still order."""
+    l = np.linspace(40, 90, 32, dtype=np.float32)[None].repeat(2, 0).copy()
+    l[1] = l[1, ::-1]
+    idx, w = against(l, 4, np.zeros(32, np.float32), score="sigmoid")
+    assert (idx == [0, 1, 2, 3]).all() and (w == 0.25).all()
+    idx, w = against(l, 4, score="sigmoid")
+    assert idx.tolist() == [[31, 30, 29, 28], [0, 1, 2, 3]] and (w == 0.25).all()
+
+
 def test_masked_experts_and_empty_rows():
     rng, l = logits(12, 48, 3)
     low = np.finfo(np.float32).min

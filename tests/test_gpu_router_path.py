@@ -48,6 +48,28 @@ def test_quantized_rows_move_unchanged(T, H, K, offset):
                           permute_ref(scale.numpy(), row.numpy(), held_s.view(torch.int32).numpy()))
 
 
+@pytest.mark.parametrize("words", [0, 1, 3, 8, 700])
+def test_rows_with_any_number_of_scale_words(words):
+    """The C call moves as many words a row as it is told: none, other groups' scales."""
+    from combine_ep_send_amd import _lib
+
+    g = torch.Generator().manual_seed(words)
+    T, H, K, cap = 37, 256, 3, 130
+    q = codes(g, T, H)
+    scale = torch.randint(-(1 << 31), 1 << 31, (T, words), generator=g).int()
+    row = torch.randperm(cap, generator=g)[:T * K].view(T, K).int()
+    held_q, held_s = codes(g, cap, H), torch.full((cap, words), 5, dtype=torch.int32)
+    dq, ds, dr, out, out_s = (t.cuda() for t in (q, scale, row, held_q, held_s))
+    st = _lib.lib().ep_dispatch_permute_quantized(
+        dq.data_ptr(), ds.data_ptr() if words else None, words, T, H, dr.data_ptr(), K, cap,
+        out.data_ptr(), out_s.data_ptr() if words else None,
+        torch.cuda.current_stream().cuda_stream)
+    assert st == _lib.EP_OK
+    assert np.array_equal(out.cpu().numpy(), permute_ref(q.numpy(), row.numpy(), held_q.numpy()))
+    assert np.array_equal(out_s.cpu().numpy(),
+                          permute_ref(scale.numpy(), row.numpy(), held_s.numpy()))
+
+
 def test_quantized_rows_past_one_launch():
     """128 channels a row: 33.6 M tokens take two launches of 2^32 - 1 work-items."""
     T = (1 << 25) + 1001
