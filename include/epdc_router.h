@@ -162,15 +162,17 @@ typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score_t;
  * Scores, keys and weights are computed in 64 bits and a weight is rounded
  * once to fp32.  Keys that agree in their first 42 bits count as equal (43
  * significant bits, the last cut off), and so do worths that agree to 2^-40;
- * the lowest index wins.  Without a bias, and with one group or group_top 1,
- * the logits themselves are compared, which orders alike, and exactly.
+ * the lowest index wins.  All groups staying (topk_groups == num_groups) is one
+ * group.  Without a bias, and with one group or group_top 1, the logits themselves
+ * are compared, which orders alike, and exactly.
  *
  * An expert is not chosen where its logit is NaN or -infinity, or its key is.
  * A slot that finds no expert has id -1 and weight 0, which the dispatch takes
  * as unrouted; a group with fewer eligible experts than group_top is worth the
  * sum of those it has, and one with none does not stay.  A NaN or +infinity
  * among the logits makes a softmax's scores NaN, and so its keys where it is
- * keys that are compared.
+ * keys that are compared; where logits are, renormalised weights come from the
+ * chosen logits alone, and are NaN only where one of these is +infinity.
  *
  *   logits        [T,E] fp32 in; E <= EPDC_MAX_BINS
  *   bias          [E] fp32 in, or NULL
