@@ -29,7 +29,10 @@ inline NormShape norm_shape(int H) {
 
 // Workgroups of the backward pass, each with one row of partial sums of the
 // weight's gradient: as many as the chip holds at once, by the waves that the
-// kernel's registers allow a compute unit.
+// kernel's registers allow a compute unit, and four a compute unit at most.  In us,
+// the sums' launch included, with two, four and eight: 16384 rows of 512 channels 33,
+// 25 and 27, of 2048 62, 60 and 66; of 4096, where three fit, 94 with two and 104; 2500
+// of 5120 26 and 29.
 inline int norm_groups(int64_t T, int H) {
   const NormShape n = norm_shape(H);
   const int waves = n.pieces == 1 ? 24 : n.pieces == 2 ? 16 : 8;
@@ -37,7 +40,9 @@ inline int norm_groups(int64_t T, int H) {
   if (per_cu < 1) per_cu = 1;
   if (per_cu > 4) per_cu = 4;
   const int most = 256 * per_cu;
-  // two rows or more each: a row of sums costs as much to move as a row
+  // two rows or more each: a row of sums costs as much to move as a row.  With one,
+  // two and eight rows: 64 rows of 4096 channels 7.0, 7.5 and 14 us, 300 11.2, 9.6 and
+  // 15.8, 1237 of 2056 18, 16 and 17
   const int64_t want = (T + 1) / 2;
   return int(want < most ? want : most);
 }
@@ -82,7 +87,17 @@ constexpr int64_t route_row(int64_t t, int64_t live) { return t < live ? t : liv
 constexpr int kGemmGroups = 256;      // workgroups that fill the chip
 
 // Logits: a workgroup takes bm tokens and 64 * wn experts over `each` stages of
-// 64 channels.
+// 64 channels; the channels are split over workgroups, whose sums a second launch adds
+// up, as long as these do not outnumber the compute units (where they may, by less
+// than one split: 8195 tokens, 64 experts, 4096 channels 23 us instead of 21, 12000 33
+// instead of 27).
+//
+// The wide form from 129 experts and 2048 tokens on.  Wide and not, in us: 256 experts
+// of 7168 channels 1024 tokens 24 and 22, 2048 26 and 26, 4096 33 and 37, 16384 87 and
+// 105; 1024 experts of 4096 channels 1024 tokens 33 and 29, 2048 40 and 42, 8192 73 and
+// 115.  160 experts of 4096 channels take 22 and 19 at 2048 tokens, 32 and 37 at 8192,
+// 256 of 1024 channels 25 and 24 at 8192; 128 experts 66 and 64 (16384 tokens of 7168
+// channels), 27 and 31 (8195 of 4096), 23 and 18 (2048 of 7168).
 struct LogitsShape {
   int bm, wn;
   int64_t mb;
@@ -112,7 +127,12 @@ inline LogitsShape logits_shape(int64_t T, int E, int H) {
 }
 
 // The rows' gradient: a workgroup keeps 16 * mt tokens' rows of dlogits in LDS,
-// 64 KB of them, and takes `each` blocks of 64 channels.
+// 64 KB of them, and takes `each` blocks of 64 channels: four, one a wave, or more, and
+// so many that two workgroups a compute unit are not passed.  Both gradients in us, with
+// one, four and eight blocks at least: 64 tokens, 64 experts, 4096 channels 13.0, 13.4
+// and 14.8, 300 x 160 x 5120 30, 30 and 33, many tokens alike; with one, two and four
+// workgroups a compute unit: 8195 x 64 x 4096 57, 51 and 51, 4096 x 256 x 7168 97, 94 and
+// 102.
 struct DxShape {
   int mt;
   int64_t mb;
@@ -135,7 +155,9 @@ inline DxShape dx_shape(int64_t T, int H, int Ep) {
 }
 
 // The weights' gradient: a workgroup takes 64 experts and 128 channels over
-// `each` steps of 32 tokens.
+// `each` steps of 32 tokens: four, one a wave, or more.  Both gradients in us, with two,
+// four and eight at least: 512 tokens, 64 experts, 4096 channels 22, 20 and 20, 300 x 160 x
+// 5120 30, 30 and 25, from 1024 tokens on alike.
 struct DwShape {
   int eb, hb, splits;
   int64_t each;
