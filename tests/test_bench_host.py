@@ -3,6 +3,8 @@ touching one, and its algorithmic byte counts (the numerator of every GB/s
 figure and of the roofline) equal the sizes of the arrays each call must read
 and write, counted here from the oracle's outputs on small workloads."""
 
+import glob
+import json
 import os
 import subprocess
 import sys
@@ -130,3 +132,18 @@ def test_chunk_streams_start_on_the_callers_stream(C, S):
     assert idx[0] == 0
     assert all(0 <= v < S for v in idx)
     assert all(idx[i + 1] == (idx[i] + 1) % S for i in range(C - 1))
+
+
+def test_measured_traffic_is_of_these_sources():
+    """bench.py reports the HBM bytes of a launch only where they were measured on the
+    library's sources as they are: every record is, so a change of the sources takes the
+    counters anew."""
+    records = glob.glob(os.path.join(ROOT, "profiles", "traffic_*.json"))
+    assert len(records) == 21
+    for path in records:
+        with open(path) as f:
+            rec = json.load(f)
+        assert os.path.basename(path) == f"traffic_{rec['workload']}_{rec['kernel']}.json"
+        assert rec["source_sha256"] == B.kernel_source_digest(), path
+        assert B.traffic_from_profiles(rec["workload"], rec["kernel"],
+                                           B.kernel_source_digest()) == rec
