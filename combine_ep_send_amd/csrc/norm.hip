@@ -12,9 +12,12 @@ constexpr int64_t kNormMaxGrid = 1 << 20;       // rows past it come round again
 
 template <typename F>
 __device__ __forceinline__ F wave_sum(F v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v += partner<0>(v);
+  v += partner<1>(v);
+  v += partner<2>(v);
+  v += partner<3>(v);
+  v += partner<4>(v);
+  return v + partner<5>(v);
 }
 
 // Sum over the workgroup, the same in every thread: lanes first, then waves in
@@ -30,6 +33,16 @@ __device__ __forceinline__ F block_sum(F v, F* part) {
   F s = 0;
   for (int w = 0; w < waves; ++w) s += part[w];
   return s;
+}
+
+// 1 / sqrt(x), x >= 0: the hardware's estimate and two of Newton's steps, which 0 and
+// infinity would turn into NaN.
+__device__ __forceinline__ double inverse_root(double x) {
+  const double r = __builtin_amdgcn_rsq(x);
+  if (!(x > 0.0 && x < INFINITY)) return r;
+  const double h = 0.5 * x;
+  const double s = __builtin_fma(r, __builtin_fma(-h * r, r, 0.5), r);
+  return __builtin_fma(s, __builtin_fma(-h * s, s, 0.5), s);
 }
 
 // Rows are written with non-temporal stores (16384 rows of 4096 channels with a
@@ -60,38 +73,42 @@ __device__ __forceinline__ void load_weight(const void* weight, int j, float (&w
   }
 }
 
-// e4m3 codes and scale of 128 values held by 16 lanes, 8 each, in 64 bits (v) and
-// rounded to fp32 (y): the rules of the dispatch's fp8 rows, the quotient rounded
-// once.  v / scale is v times 1 / scale in 64 bits, one division for the lane.  NaN is
-// left out of amax; only a lane with one, or a group with an infinity, needs the
-// encoder that knows NaN.  A quotient passes 448 by 2^-23 of it, or by more where the
-// scale is subnormal; past 464 the conversion instruction gives NaN, so the quotients
-// are clamped first, which is the saturation the codes call for.
+// e4m3 codes and scale of 128 values held by 16 lanes, 8 each, in 64 bits (v; y: the
+// same as fp32): the rules of the dispatch's fp8 rows, scale and quotient rounded once.
+// Scaled values lie on the border of two codes about once in 10^4, where the scale's
+// rounding decides: with the largest value rounded to fp32 before its division, 26 % of
+// the scales and one code in 20000 came out as the neighbour.  v / scale is v times
+// 1 / scale in 64 bits, one division for the lane.  NaN is left out of amax; only a lane
+// with one, or a group with an infinity, needs the encoder that knows NaN.  A quotient
+// passes 448 by 2^-24 of it, or by more where the scale is subnormal; past 464 the
+// conversion instruction gives NaN, so the quotients are clamped first, which is the
+// saturation the codes call for.
 __device__ __forceinline__ u32x2 quantize_group(const double (&v)[8], const float (&y)[8],
                                                 bool pow2, float& scale) {
-  uint32_t m = 0u;
+  double m = 0.0;
+  float sum = 0.0f;                        // NaN where a value is (or infinities cancel)
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-  const bool lane_nan = m > 0x7F800000u;
-  if (lane_nan) {
-    m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t u = __float_as_uint(y[i]) & 0x7FFFFFFFu;
-      if (u <= 0x7F800000u) m = max(m, u);
-    }
+  for (int i = 0; i < 8; ++i) {
+    m = fmax(m, fabs(v[i]));
+    sum += y[i];
   }
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
-  scale = __uint_as_float(m) / 448.0f;
+  m = fmax(m, partner<0>(m));
+  m = fmax(m, partner<1>(m));
+  m = fmax(m, partner<2>(m));
+  m = fmax(m, partner<3>(m));
+  // m / 448: the product with the inverse, and what is left of m
+  const double part = m * (1.0 / 448.0);
+  scale = m < INFINITY
+              ? float(__builtin_fma(__builtin_fma(-448.0, part, m), 1.0 / 448.0, part))
+              : INFINITY;
   if (pow2) scale = pow2_ceil(scale);
-  if (!lane_nan && m != 0x7F800000u) {
+  if (sum == sum && m < INFINITY) {
     if (scale == 0.0f) return u32x2{0u, 0u};
-    const double inverse = 1.0 / double(scale);
+    const double by = inverse(double(scale));
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      t[i] = __builtin_amdgcn_fmed3f(float(v[i] * inverse), -448.0f, 448.0f);
+      t[i] = __builtin_amdgcn_fmed3f(float(v[i] * by), -448.0f, 448.0f);
     u32x2 c;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -100,29 +117,31 @@ __device__ __forceinline__ u32x2 quantize_group(const double (&v)[8], const floa
     }
     return c;
   }
-  const double inverse = 1.0 / double(scale);
+  const double by = 1.0 / double(scale);
   uint32_t c[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    c[i] = scale > 0.0f ? e4m3_encode(float(v[i] * inverse)) : (y[i] != y[i] ? 0x7Fu : 0u);
+    c[i] = scale > 0.0f ? e4m3_encode(float(v[i] * by)) : (v[i] != v[i] ? 0x7Fu : 0u);
   return u32x2{c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
                c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24)};
 }
 
 // ---------------------------------------------------------------------------
 // Forward: one workgroup a row, the row in registers between the sum of squares
-// and the output, so that every byte moves once.  The squares of eight neighbours
-// add up in fp32, the rest of the row's sum in 64 bits (all of it there: 205 against
-// 185 us), and the values that become codes (Q) are in 64 bits, at the same speed (a
-// value that goes to bf16 alone is in fp32).  16384 rows of 7168 channels with residual and codes: 171 to
-// 195 us (1061 MB, 5.4 to 6.2 TB/s).  A thread's pieces lie a
-// workgroup apart: consecutive threads move consecutive 16-byte pieces, and 16
-// neighbours hold a 128-channel group.
+// and the output, so that every byte moves once.  The squares of two neighbours add up
+// in fp32, the rest of the row's sum in 64 bits, as are the values that become codes
+// (Q): of 117 million codes about 35 then are not those of 64 bits throughout (eight
+// neighbours: 590, at 169 instead of 170 us; all squares in 64 bits: none, at 177).  A
+// value that goes to bf16 alone is in fp32.  16384 rows of 7168 channels with residual and
+// codes: 170 to 195 us (1061 MB, 5.4 to 6.2 TB/s).  A thread's pieces lie a workgroup
+// apart: consecutive threads move consecutive 16-byte pieces, and 16 neighbours hold a
+// 128-channel group.
 // ---------------------------------------------------------------------------
 template <int PT, bool W32, bool NT, bool Q>
 __global__ __launch_bounds__(kNormMaxThreads) void rms_norm_kernel(NormArgs a) {
   __shared__ double part[2][kNormMaxWaves];
   const int H8 = a.H >> 3, n = int(blockDim.x);
+  const double by_h = 1.0 / double(a.H);
   int turn = 0;
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
     const u32x4* x = static_cast<const u32x4*>(a.x) + t * H8;
@@ -157,11 +176,11 @@ __global__ __launch_bounds__(kNormMaxThreads) void rms_norm_kernel(NormArgs a) {
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
-      float f[8], s = 0.0f;
+      float f[8];
       unpack8(v[i], f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s = __builtin_fmaf(f[k], f[k], s);
-      sum += double(s);
+      for (int k = 0; k < 8; k += 2)
+        sum += double(__builtin_fmaf(f[k + 1], f[k + 1], f[k] * f[k]));
     }
     sum = block_sum(sum, part[turn]);
     // Squares that fp32 does not hold are taken once more in 64 bits: below 2^-100 for the
@@ -182,7 +201,7 @@ __global__ __launch_bounds__(kNormMaxThreads) void rms_norm_kernel(NormArgs a) {
       }
       sum = block_sum(sum, part[turn]);
     }
-    const double rstd = 1.0 / sqrt((sum + all_eps) / double(a.H));
+    const double rstd = inverse_root((sum + all_eps) * by_h);
     if (a.rstd && threadIdx.x == 0) a.rstd[t] = float(rstd);
     // without codes y is in fp32; the least rows' rstd, up to 2^141, is past it
     const float lift = rstd > 0x1p120 ? 0x1p21f : 1.0f;

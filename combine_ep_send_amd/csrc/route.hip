@@ -15,7 +15,7 @@
 // The vector unit bounds it: 16384 tokens, 256 experts in 8 groups, sigmoid and bias
 // take 16 us, 1640 instructions a wave of four tokens (18 MB: 3 us of memory); by
 // logits alone 9 us, 64 experts 7.
-#include "epdc_device.h"
+#include "router_device.h"
 #include "router_launch.h"
 
 namespace epdc {
@@ -44,25 +44,6 @@ __device__ __forceinline__ int expert_of(double key) {
   const uint64_t b = __builtin_bit_cast(uint64_t, key);
   const int c = int(uint32_t(b) & kIndexBits);
   return (b >> 63) ? c : int(kIndexBits) - c;
-}
-
-// The value of the partner lane at each step of a join over 2, 4, 8, 16, 32, 64
-// lanes: after a step all lanes of the block hold the same, so any pairing of
-// the two halves does.  Within 16 lanes by data-parallel moves.
-template <int STEP>
-__device__ __forceinline__ int partner(int v) {
-  if constexpr (STEP == 0) return __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xF, 0xF, false);
-  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xF, 0xF, false);
-  if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xF, 0xF, false);
-  if constexpr (STEP == 3) return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xF, 0xF, false);
-  return __shfl_xor(v, 1 << STEP);
-}
-template <int STEP>
-__device__ __forceinline__ double partner(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = uint32_t(partner<STEP>(int(uint32_t(b))));
-  const uint32_t hi = uint32_t(partner<STEP>(int(uint32_t(b >> 32))));
-  return __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
 }
 
 __device__ __forceinline__ double from_lane(double v, int lane) {
@@ -214,12 +195,6 @@ __device__ __forceinline__ double exp_within(double x) {
 // The same for any x <= 0.
 __device__ __forceinline__ double exp_down(double x) {
   return exp_within(x < -800.0 ? -800.0 : x);
-}
-// 1 / y for y in [1, 2]: the hardware's estimate and two of Newton's steps.
-__device__ __forceinline__ double inverse(double y) {
-  double r = __builtin_amdgcn_rcp(y);
-  r = __builtin_fma(r, __builtin_fma(-y, r, 1.0), r);
-  return __builtin_fma(r, __builtin_fma(-y, r, 1.0), r);
 }
 
 // From exp(-|l|), without cancellation on either side.  The first is for logits

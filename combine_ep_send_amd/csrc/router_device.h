@@ -5,6 +5,37 @@
 
 namespace epdc {
 
+// The value of the partner lane at each step of a join over 2, 4, 8, 16, 32, 64
+// lanes: after a step all lanes of the block hold the same, so any pairing of
+// the two halves does.  Within 16 lanes by data-parallel moves.
+template <int STEP>
+__device__ __forceinline__ int partner(int v) {
+  if constexpr (STEP == 0) return __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xF, 0xF, false);
+  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xF, 0xF, false);
+  if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xF, 0xF, false);
+  if constexpr (STEP == 3) return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xF, 0xF, false);
+  return __shfl_xor(v, 1 << STEP);
+}
+template <int STEP>
+__device__ __forceinline__ double partner(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = uint32_t(partner<STEP>(int(uint32_t(b))));
+  const uint32_t hi = uint32_t(partner<STEP>(int(uint32_t(b >> 32))));
+  return __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
+}
+
+template <int STEP>
+__device__ __forceinline__ float partner(float v) {
+  return __int_as_float(partner<STEP>(__float_as_int(v)));
+}
+
+// 1 / y, both in the normal range: the hardware's estimate and two of Newton's steps.
+__device__ __forceinline__ double inverse(double y) {
+  double r = __builtin_amdgcn_rcp(y);
+  r = __builtin_fma(r, __builtin_fma(-y, r, 1.0), r);
+  return __builtin_fma(r, __builtin_fma(-y, r, 1.0), r);
+}
+
 // out[c] = sum over r of part[r][c], rows of `columns` floats: a wave takes 64
 // columns, one a lane, and rows r, r + along, ... of them, `along` waves of a
 // workgroup side by side; their sums then add up in order.  The order depends on

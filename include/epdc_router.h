@@ -45,9 +45,9 @@ typedef enum { EP_NORM_W_BF16 = 0, EP_NORM_W_F32 = 1 } ep_norm_weight_t;
  *   y[t,h]  = s[t,h] * rstd[t] * weight[h]
  *   out     = bf16(fp32(y))
  *   q, scale: e4m3 codes and one scale per 128 channels of y, not of out: amax =
- *             max |fp32(y)|, scale = fp32(amax / 448), or the smallest power of
- *             two at or above that, code = e4m3(fp32(y / scale)).
- * rstd is in 64 bits, from fp32 sums of the squares of eight neighbours, or from 64-bit
+ *             max |y|, scale = fp32(amax / 448), or the smallest power of two at or
+ *             above that, code = e4m3(fp32(y / scale)).
+ * rstd is in 64 bits, from fp32 sums of the squares of two neighbours, or from 64-bit
  * squares where fp32 does not hold the row's (below 2^-100 with H * eps, or past its
  * largest); y is in 64 bits where there are codes, in fp32 without.  The rstd that is
  * written is infinite where fp32 cannot hold it: rows whose root mean square lies below

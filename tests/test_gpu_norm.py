@@ -64,6 +64,37 @@ def test_codes_and_scales(T, H, fmt, f32):
     check(v, y.reshape(v.shape), step * (1 + 1e-5) + tol.reshape(v.shape), "codes")
 
 
+@pytest.mark.parametrize("fmt", ["f32", "pow2"])
+@pytest.mark.parametrize("f32", [False, True])
+def test_codes_are_the_roundings_of_64_bits(fmt, f32):
+    """Whole numbers, whose squares' sums are exact: y is off by rounding in 64 bits alone,
+    2^-50 of it, so scale and codes are the formula's roundings, unless a value lies
+    within 2^-49 of a border.  About one value in 10^4 lies on the border of two codes
+    but for the scale's rounding, so a scale one fp32 step off would show in codes."""
+    rng = np.random.default_rng(17)
+    T, H = 200, 1024
+    x = rng.integers(-15, 16, (T, H)).astype(np.float64)
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(H))
+    w = w.float() if f32 else w.to(torch.bfloat16)
+    n = ep.ep_rms_norm(bf16(x).cuda(), w.cuda(), 1e-6, fp8=True, scale_fmt=fmt)
+    y = x / np.sqrt((x * x).mean(1, keepdims=True) + float(np.float32(1e-6))) * f64(w)
+    y = y.reshape(T, -1, 128)
+    ends = (1 - 2.0 ** -49, 1 + 2.0 ** -49)
+    lo, hi = ((np.abs(y).max(-1) / 448 * e).astype(np.float32).astype(np.float64) for e in ends)
+    if fmt == "pow2":
+        lo, hi = (2.0 ** np.ceil(np.log2(v)) for v in (lo, hi))
+    scale = f64(n.scale)
+    assert ((lo <= scale) & (scale <= hi)).all() and (lo == hi).mean() > 0.99
+
+    def code(v):
+        v = np.clip(v, -448, 448).astype(np.float32)
+        return torch.from_numpy(v).to(torch.float8_e4m3fn).double().numpy()
+    lo, hi = (code(y / scale[..., None] * e) for e in ends)
+    got = f64(n.q.float()).reshape(y.shape)
+    assert ((np.minimum(lo, hi) <= got) & (got <= np.maximum(lo, hi))).all()
+    assert (lo == hi).mean() > 0.999
+
+
 def test_codes_are_those_of_the_dispatch():
     """Rows that need no rounding on the way: signs times a power of two, rstd and
     weight powers of two, so that bf16 holds y and both quantizers see the same."""
