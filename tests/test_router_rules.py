@@ -3,11 +3,13 @@ them: host arithmetic, so no GPU is needed."""
 
 import ctypes
 import os
+import re
 import shutil
 import subprocess
 
 import pytest
 
+from combine_ep_send_amd import build
 from tests.expert_forms import CSRC
 from tests.router_forms import DEEP
 
@@ -18,6 +20,10 @@ RULES = r"""
 using namespace epdc;
 extern "C" int64_t live(int64_t T, int64_t count) { return route_live(T, count); }
 extern "C" int64_t row(int64_t t, int64_t live) { return route_row(t, live); }
+extern "C" int norm(int64_t T, int H, int* f) {
+  f[0] = norm_shape(H).pieces, f[1] = norm_shape(H).threads;
+  return norm_groups(T, H);
+}
 extern "C" void forms(int64_t T, int E, int H, int64_t* f) {
   const LogitsShape g = logits_shape(T, E, H);
   f[0] = g.wide, f[1] = g.bm, f[2] = g.wn, f[3] = g.nb, f[4] = g.each, f[5] = g.splits;
@@ -41,6 +47,7 @@ def rules(tmp_path_factory):
     for name in ("live", "row"):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int64, [ctypes.c_int64, ctypes.c_int64]
+    lib.norm.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_void_p]
     lib.forms.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]
     return lib
 
@@ -85,3 +92,26 @@ def test_no_logits_of_padding_are_read(rules, tokens):
                     continue                         # such a workgroup reads none
                 for t in range(t0, t0 + tokens):
                     assert rules.row(t, live) == (t if t < live else live - 1)
+
+
+@pytest.mark.skipif(not os.path.exists(build.hipcc()), reason="hipcc not found")
+def test_the_chip_holds_the_norms_backward_workgroups_at_once(rules, tmp_path):
+    """The waves a compute unit that norm_groups counts on, by the registers of the kernels
+    as the compiler reports them: as many workgroups as fit, four at most."""
+    flags = [f for f in build.HIPCC_FLAGS if f != "-shared"]
+    out = subprocess.run([build.hipcc(), *flags, "-I", os.path.join(build.ROOT, "include"),
+                          "-Rpass-analysis=kernel-resource-usage", "--cuda-device-only", "-c", "-o",
+                          str(tmp_path / "norm.o"), os.path.join(CSRC, "norm.hip")],
+                         capture_output=True, text=True, check=True).stderr
+    waves = {}
+    for name, simd in re.findall(r"Function Name: (\S+).*?Occupancy \[waves/SIMD\]: (\d+)", out,
+                                 re.S):
+        m = re.search(r"rms_norm_backward_kernelILi(\d)E", name)
+        if m:
+            waves.setdefault(int(m.group(1)), set()).add(4 * int(simd))
+    assert set(waves) == {1, 2, 4, 8} and all(len(v) == 1 for v in waves.values()), waves
+    for H in (8, 520, 1032, 2056, 2560, 4096, 4104, 5120, 7168, 8192, 12288, 16384, 24576, 32768):
+        f = (ctypes.c_int * 2)()
+        each = rules.norm(1 << 29, H, f) // 256
+        fit = next(iter(waves[f[0]])) // (f[1] // 64)
+        assert each == max(1, min(4, fit)), (H, each, fit)
