@@ -348,9 +348,9 @@ __global__ __launch_bounds__(kBlock) void route_kernel(RouteArgs a, int width, b
   if (a.renorm) total = over_lanes<16>(s, add);
   if (t >= a.T || li >= a.K) return;
   a.topk_idx[t * a.K + li] = e;
-  // no sum: no weights
+  // no sum: no weights.  The quotient first: least scores times a small scale would be 0
   a.topk_weights[t * a.K + li] =
-      chosen && total != 0.0 ? float(double(a.scale) * s / total) : 0.0f;
+      chosen && total != 0.0 ? float(double(a.scale) * (s / total)) : 0.0f;
 }
 
 // ---------------------------------------------------------------------------

@@ -277,6 +277,21 @@ def test_backward_of_sigmoids_near_the_least_number(top):
     check(got, ref, F32 * np.abs(ref) + (2.0 ** -44 + 4 * least) * size + SMALL)
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -30, 1e-3, 1.0, 2.5])
+@pytest.mark.parametrize("top", [-700.0, -712.0, -735.0])
+def test_weights_of_sigmoids_near_the_least_number(top, scale):
+    """Renormalised weights of scores that 64 bits only just hold, scaled up and down:
+    the scale takes no bits from them.  A score's rounding as in the test above."""
+    rng = np.random.default_rng(int(-top))
+    l = (top - 4.0 * rng.random((9, 24))).astype(np.float32)
+    idx, w = run(l, 5, score="sigmoid", scale=scale)
+    assert np.array_equal(idx, np.argsort(-l, axis=1, kind="stable")[:, :5])
+    at = np.take_along_axis(l, idx, 1).astype(np.float64)
+    q = np.exp(at - at[:, :1])
+    q *= float(np.float32(scale)) / q.sum(1, keepdims=True)
+    check(w, q, (F32 + 2.0 ** -44 + 2 * 2.0 ** -1074 / np.exp(top - 4.0)) * q, "weights")
+
+
 def test_arrays_aligned_to_four_bytes():
     """Logits and bias off by a float: the loads of fours need 16 bytes."""
     rng, l = logits(50, 64, 2)
