@@ -39,7 +39,8 @@ def test_examples_run():
     factor = 2.0 ** np.arange(-1, 3)[np.arange(32) % 4]
 
     def by():
-        return torch.from_numpy(factor).cuda()[have["handle"].send_rank.long() % 32, None].bfloat16()
+        rank = have["handle"].send_rank.long() % 32
+        return torch.from_numpy(factor).cuda()[rank, None].bfloat16()
     have.update(residual=rows(T, H), weight=torch.ones(H).cuda(), gate=rows(E, H, by=H ** -0.5),
                 bias=torch.zeros(E).cuda(), d_out=rows(T, H),
                 expert_fp8=lambda recv, *_: codes_to_bf16(recv) * by(),
